@@ -24,7 +24,8 @@ DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 __all__ = ["gattn_prefill", "gattn_prefill_varlen", "gattn_decode", "gattn_decode_append", "gattn_decode_paged", "gattn_decode_noalloc", "gattn_prefill_workspace_size", "gattn_prefill_varlen_workspace_size", "gattn_decode_workspace_size",
            "gattn_get_device_status", "gattn_set_profile_events", "gattn_selftest_wait_timeout", "gattn_o_proj", "gattn_strerror", "GattnError", "GATE_MODES",
-           "GATE_ACTS", "GATE_ADDITIVE"]
+           "GATE_ACTS", "GATE_ADDITIVE", "gattn_qcache_shape", "gattn_qcache_write", "gattn_qcache_read",
+           "gattn_decode_qcache", "gattn_decode_qcache_workspace_size"]
 
 
 def _ptr(t):
@@ -341,4 +342,196 @@ def gattn_decode_noalloc(q_new, kv_cache, seqlens, gate, qnorm_w, *, rotary_dim,
         _ptr(q_new), _ptr(kv_cache), _ptr(seqlens), _ptr(gate if mode & 0x0F else None), _ptr(qnorm_w), B, H, G, d,
         Lmax, int(rotary_dim), float(rope_base), float(eps), mode, _ptr(out), _stream_handle(stream, q_new.device))
     check(st, "gattn_decode_noalloc")
+    return out
+
+
+# ------------------------------------------------------------------ 4-bit KV cache
+
+def gattn_qcache_shape(num_pages, G, page_size, d):
+    """Shape of a 4-bit KV cache, a uint8 tensor [2, num_pages, G, page_size/16, 10 d] (the
+    layout is in gattn.h).  It needs no initialisation."""
+    if page_size < 16 or page_size % 16 or d not in (64, 128, 256):
+        raise ValueError("page_size must be a multiple of 16 and d one of 64, 128, 256")
+    return (2, num_pages, G, page_size // 16, 10 * d)
+
+
+def _qcache_geometry(qcache, block_table, B):
+    """(num_pages, G, page_size, d, max_pages) of a cache and its table, checked."""
+    if qcache.dim() != 5 or qcache.shape[0] != 2 or qcache.dtype != torch.uint8 or not qcache.is_contiguous():
+        raise ValueError("qcache must be a contiguous uint8 [2,num_pages,G,page_size/16,10 d] tensor")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [B,max_pages] tensor")
+    if block_table.shape[0] != B or block_table.device != qcache.device:
+        raise ValueError(f"block_table must have one row for each of {B} sequences, on the cache's device")
+    _, num_pages, G, blocks, row = qcache.shape
+    if row % 10:
+        raise ValueError("qcache: the last dimension is 10 d bytes")
+    return num_pages, G, 16 * blocks, row // 10, block_table.shape[1]
+
+
+def _qcache_index(name, t, n, device):
+    if t.dim() != 1 or t.shape[0] != n or t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} on the cache's device")
+    return t.data_ptr()
+
+
+def _qcache_stride(t, i, name):
+    """Stride of dimension i for the C call, where 0 selects the contiguous default: a
+    dimension of one has no stride to speak of, and a broadcast one cannot be passed."""
+    if t.shape[i] <= 1:
+        return 0
+    if t.stride(i) == 0:
+        raise ValueError(f"{name}: broadcast (stride 0) views are not supported; pass a contiguous copy")
+    return t.stride(i)
+
+
+def _qcache_call(device, stream, fn, *args):
+    """fn(*args, stream handle) with the tensors' device current."""
+    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        return fn(*args, s)
+    with torch.cuda.device(device):
+        return fn(*args, s)
+
+
+def _empty_on(stream, shape, dtype, device):
+    """torch.empty whose memory belongs to the stream that will use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def gattn_qcache_write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens=None, *, rotary_dim, rope_base, eps=1e-6,
+                       stream=None):
+    """Write new tokens into a 4-bit KV cache (gattn_qcache_shape) in place and return it.
+
+    k, v [T,G,d] raw projections, bf16 or fp32, the last dimension contiguous (views into
+    a fused projection are fine); knorm_w [d] of the same dtype; K is normed and rotated.
+    cu_seqlens [B+1] int32 on the device: sequence b's new tokens are rows cu_seqlens[b] ..
+    cu_seqlens[b+1]-1 (rows past the last are ignored); None: one token per sequence.
+    seqlens [B] int32 on the device: tokens in each sequence after the write.
+    block_table [B,max_pages] int32: the page of each page_size-token stretch."""
+    if k.dim() != 3 or v.shape != k.shape or k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("k and v must be [T,G,d] with a contiguous last dimension")
+    if k.dtype not in DTYPES or v.dtype != k.dtype or knorm_w.dtype != k.dtype:
+        raise ValueError("k, v and knorm_w must all be bfloat16 or all be float32")
+    T, G, d = k.shape
+    B = seqlens.shape[0]
+    num_pages, cG, page_size, cd, max_pages = _qcache_geometry(qcache, block_table, B)
+    device = qcache.device
+    if (cG, cd) != (G, d) or knorm_w.shape != (d,) or not knorm_w.is_contiguous():
+        raise ValueError(f"the cache holds {cG} heads of {cd}, k and v {G} of {d}; knorm_w must be a contiguous [{d}]")
+    if k.device != device or v.device != device or knorm_w.device != device:
+        raise ValueError("k, v, knorm_w and the cache must be on one device")
+    if cu_seqlens is None and T != B:
+        raise ValueError(f"without cu_seqlens every sequence gets one token: {T} tokens, {B} sequences")
+    ks, kh, vs, vh = (_qcache_stride(t, i, "k, v") for t in (k, v) for i in (0, 1))
+    st = _qcache_call(
+        device, stream, _lib.load().gattn_qcache_write, k.data_ptr(), v.data_ptr(), qcache.data_ptr(),
+        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, device),
+        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, device), knorm_w.data_ptr(),
+        T, B, G, d, rotary_dim, rope_base, eps, ks, kh, vs, vh, DTYPES[k.dtype])
+    check(st, "gattn_qcache_write")
+    return qcache
+
+
+def gattn_qcache_read(qcache, block_table, starts=None, cu_seqlens=None, *, total=None, dtype=torch.bfloat16,
+                      k_out=None, v_out=None, stream=None):
+    """Read cached tokens back: (k, v), each [total,G,d] in `dtype` (bf16 or fp32), K as the
+    cache holds it (normed and rotated).
+
+    Rows cu_seqlens[b] .. cu_seqlens[b+1]-1 receive the tokens starts[b], starts[b]+1, ... of
+    sequence b; both are int32 on the device.  cu_seqlens None: one token per sequence
+    (total = B); starts None: from token 0.  total is the number of rows, cu_seqlens[B] or
+    more (rows past it are left as they were).  k_out, v_out: contiguous tensors to fill."""
+    B = block_table.shape[0]
+    num_pages, G, page_size, d, max_pages = _qcache_geometry(qcache, block_table, B)
+    device = qcache.device
+    if total is None:
+        total = B if cu_seqlens is None else None if k_out is None else k_out.shape[0]
+    if total is None:
+        raise ValueError("total (the number of rows) is needed with cu_seqlens")
+    if cu_seqlens is None and total != B:
+        raise ValueError("without cu_seqlens one token of each sequence is read")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        if dtype not in DTYPES:
+            raise ValueError("dtype must be bfloat16 or float32")
+        k_out = _empty_on(stream, (total, G, d), dtype, device)
+        v_out = _empty_on(stream, (total, G, d), dtype, device)
+    else:
+        for t in (k_out, v_out):
+            if t.shape != (total, G, d) or t.dtype not in DTYPES or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"k_out and v_out must be contiguous bf16 or fp32 [{total},{G},{d}] tensors")
+        if k_out.dtype != v_out.dtype:
+            raise ValueError("k_out and v_out must have one dtype")
+    st = _qcache_call(
+        device, stream, _lib.load().gattn_qcache_read, qcache.data_ptr(), block_table.data_ptr(), num_pages, page_size,
+        max_pages, None if starts is None else _qcache_index("starts", starts, B, device),
+        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, device), total, B, G, d,
+        DTYPES[k_out.dtype], k_out.data_ptr(), v_out.data_ptr())
+    check(st, "gattn_qcache_read")
+    return k_out, v_out
+
+
+def gattn_decode_qcache_workspace_size(B, H, G, d, Lmax) -> int:
+    return _lib.load().gattn_decode_qcache_workspace_size(B, H, G, d, Lmax)
+
+
+def gattn_decode_qcache(q_new, qcache, block_table, seqlens, gate, qnorm_w, *, rotary_dim, rope_base, eps=1e-6,
+                        k_new=None, v_new=None, knorm_w=None, gate_mode="elementwise", gate_act="sigmoid",
+                        gate_additive=False, out=None, workspace=None, stream=None):
+    """One decode step against a 4-bit KV cache (gattn_qcache_shape): q_new [B,H,d] raw bf16
+    queries and gate logits [B,H,d], [B,H], [B,d] or None, both possibly strided views with
+    a contiguous last dimension (e.g. the halves of a packed [B,H,2d] projection).
+    seqlens [B] int32 counts the new token; 0 marks an unused row.  With k_new, v_new
+    [B,G,d] and knorm_w the new token is first written into the cache.  The rest as
+    gattn_decode_paged.  Returns out [B,H*d]."""
+    mode = _mode(gate_mode, gate_act, gate_additive)
+    if q_new.dim() != 3 or q_new.stride(2) != 1 or q_new.dtype != torch.bfloat16:
+        raise ValueError("q_new must be a bfloat16 [B,H,d] tensor with a contiguous last dimension")
+    B, H, d = q_new.shape
+    num_pages, G, page_size, cd, max_pages = _qcache_geometry(qcache, block_table, B)
+    device = qcache.device
+    if cd != d or qnorm_w.shape != (d,) or qnorm_w.dtype != torch.bfloat16 or not qnorm_w.is_contiguous():
+        raise ValueError(f"head_dim: q_new {d}, cache {cd}; qnorm_w must be a contiguous bfloat16 [{d}]")
+    if q_new.device != device or qnorm_w.device != device:
+        raise ValueError("q_new, qnorm_w and the cache must be on one device")
+    layout = mode & 0x0F
+    gp, gs, gh = None, 0, 0
+    if layout:
+        want = (B, H, d) if layout == 1 else (B, H) if layout == 2 else (B, d)
+        if gate is None or gate.shape != want or gate.dtype != torch.bfloat16 or gate.device != device:
+            raise ValueError(f"gate must be a bfloat16 {list(want)} tensor on the cache's device")
+        if layout != 2 and gate.stride(-1) != 1:
+            raise ValueError("gate: the last dimension must be contiguous")
+        gp, gs = gate.data_ptr(), _qcache_stride(gate, 0, "gate")
+        gh = _qcache_stride(gate, 1, "gate") if layout != 3 else 0
+    kp = vp = wp = None
+    if k_new is not None or v_new is not None or knorm_w is not None:
+        if k_new is None or v_new is None or knorm_w is None:
+            raise ValueError("an append needs k_new, v_new and knorm_w")
+        for name, t, shape in (("k_new", k_new, (B, G, d)), ("v_new", v_new, (B, G, d)), ("knorm_w", knorm_w, (d,))):
+            if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"{name} must be a contiguous bfloat16 {list(shape)} tensor on the cache's device")
+        kp, vp, wp = k_new.data_ptr(), v_new.data_ptr(), knorm_w.data_ptr()
+    if out is None:
+        out = _empty_on(stream, (B, H * d), torch.bfloat16, device)
+    elif out.shape != (B, H * d) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"out must be a contiguous bfloat16 [{B},{H * d}] tensor on the cache's device")
+    if workspace is None:
+        with torch.cuda.device(device):
+            need = gattn_decode_qcache_workspace_size(B, H, G, d, max_pages * page_size)
+        workspace = _empty_on(stream, (max(need, 1),), torch.uint8, device)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    st = _qcache_call(
+        device, stream, _lib.load().gattn_decode_qcache, q_new.data_ptr(), kp, vp, qcache.data_ptr(),
+        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, device), gp,
+        qnorm_w.data_ptr(), wp, B, H, G, d, rotary_dim, rope_base, eps, mode, _qcache_stride(q_new, 0, "q_new"),
+        _qcache_stride(q_new, 1, "q_new"), gs, gh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        out.data_ptr())
+    check(st, "gattn_decode_qcache")
     return out

@@ -21,6 +21,11 @@ EXPORTS = (
     "gattn_set_profile_events",
     "gattn_selftest_wait_timeout",
     "gattn_o_proj",
+    "gattn_qcache_bytes",
+    "gattn_qcache_write",
+    "gattn_qcache_read",
+    "gattn_decode_qcache_workspace_size",
+    "gattn_decode_qcache",
 )
 
 _lib = None
@@ -73,6 +78,18 @@ def load():
     lib.gattn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, _vp, _vp]
     lib.gattn_o_proj.restype = _i
     lib.gattn_o_proj.argtypes = [_vp, _vp, _i, _i, _i, _vp, _vp]
+    lib.gattn_qcache_bytes.restype = _sz
+    lib.gattn_qcache_bytes.argtypes = [_i, _i, _i, _i]
+    lib.gattn_qcache_write.restype = _i
+    lib.gattn_qcache_write.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _d, _f,
+                                       _i64, _i64, _i64, _i64, _i, _vp]
+    lib.gattn_qcache_read.restype = _i
+    lib.gattn_qcache_read.argtypes = [_vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]
+    lib.gattn_decode_qcache_workspace_size.restype = _sz
+    lib.gattn_decode_qcache_workspace_size.argtypes = [_i, _i, _i, _i, _i]
+    lib.gattn_decode_qcache.restype = _i
+    lib.gattn_decode_qcache.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                        _d, _f, _i, _i64, _i64, _i64, _i64, _vp, _sz, _vp, _vp]
     lib.gattn_set_profile_events.restype = None
     lib.gattn_set_profile_events.argtypes = [_vp, _vp]
     _lib = lib

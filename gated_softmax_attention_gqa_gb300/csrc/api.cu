@@ -131,7 +131,7 @@ bool encode_bf16_map_uncached(CUtensorMap* map, const void* base, int rank, cons
 }
 
 // layout | activation | additive; no gate means no activation or combine bits either
-bool valid_gate_mode(int m) {
+bool gate_mode_ok(int m) {
     if (m < 0 || (m & ~0x1FF)) return false;
     const int layout = m & 0x0F, act = m & 0xF0;
     if (layout > GATTN_GATE_HEAD_SHARED) return false;
@@ -175,6 +175,14 @@ size_t prefill_ws(int B, int S, int H, int G, int d, int dtype) {
 }
 
 }  // namespace
+
+unsigned int* gattn::device_status_word() { return status_ptr(); }
+int gattn::device_sm_count() { return sm_count(); }
+bool gattn::valid_gate_mode(int mode) { return gate_mode_ok(mode); }
+void gattn::profile_events(cudaEvent_t* start, cudaEvent_t* stop) {
+    *start = g_prof_start;
+    *stop = g_prof_stop;
+}
 
 // Packed sequences: host copy of the cumulative sequence lengths.
 struct Varlen {

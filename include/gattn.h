@@ -301,6 +301,106 @@ gattn_status gattn_decode_noalloc(const void* q_new, const void* kv_cache, const
                                   double rope_base, float eps, int gate_mode, void* out, void* stream);
 
 /*
+ * A KV cache held in 4 bits, for decoding from long contexts: a paged pool like
+ * gattn_decode_paged's whose numbers take 5 bits (a 4-bit code, and a scale and a
+ * centre for every 32 features) instead of 16.
+ *
+ *   qcache      [2, num_pages, G, page_size / 16, 10 d] bytes, 16-byte aligned,
+ *               gattn_qcache_bytes() in all: plane 0 K normed and rotated, plane 1 raw
+ *               V.  16 consecutive tokens of one KV head are one block of 10 d bytes:
+ *                 codes   [d / 64][16 tokens][32 bytes]: 64 features of a token as
+ *                         eight little-endian 32-bit words; word w holds features
+ *                         4w .. 4w+3 in its low half and 32+4w .. 32+4w+3 in its high
+ *                         half, the lowest feature in the lowest four bits;
+ *                 scales  [d / 32][16 tokens] bf16;
+ *                 centres [d / 32][16 tokens] bf16.
+ *               A feature stands for centre + scale * (code - 8).  A group of 32
+ *               features with extremes lo and hi is written with step = (hi - lo) / 15
+ *               in fp32, scale = bf16(step), centre = bf16(lo + 8 step) and code - 8 =
+ *               (x - centre) * fp32(1 / scale) rounded half to even and clamped to
+ *               [-8, 7].  A group that holds an infinity or a NaN gets a NaN scale and
+ *               centre and reads back as NaN; one whose scale is below the smallest
+ *               normal fp32 number reads back as its centre.
+ *   block_table [B, max_pages] int32 device array, as for gattn_decode_paged: only the
+ *               entries that cover the tokens a call deals with are read.  An entry
+ *               outside [0, num_pages) sets GATTN_DEVICE_BAD_PAGE; nothing is read or
+ *               written outside the pool.
+ *   page_size   any multiple of 16 (others: GATTN_ERR_UNSUPPORTED); a sequence holds up
+ *               to Lmax = max_pages * page_size tokens.
+ *   d in {64, 128, 256}; rotary_dim a multiple of 16.
+ *
+ * Nothing of a page needs to be initialised before tokens are written to it.  Two live
+ * tokens must not share a cache row (two sequences naming one page write different
+ * rows of it, or only read it); calls that write and read the same rows are ordered by
+ * their streams.
+ */
+size_t gattn_qcache_bytes(int num_pages, int G, int page_size, int d);
+
+/*
+ * Write new tokens into the cache: K is normed (knorm_w, eps) and rotated at the
+ * token's position in its sequence, V taken as it is, and both are quantised.
+ *
+ * k, v       [T,G,d] raw projections, element (t,g,e) at k[t*k_tok_stride +
+ *            g*k_head_stride + e] (0: contiguous), so both may point into the output of
+ *            one fused projection; dtype GATTN_BF16 or GATTN_FP32, knorm_w [d] too.
+ *            Bases and strides are multiples of 16 bytes.
+ * cu_seqlens [B+1] int32 DEVICE array: sequence b's new tokens are rows
+ *            [cu_seqlens[b], cu_seqlens[b+1]), in order; 0 = cu_seqlens[0] <= ...
+ *            Rows at or past cu_seqlens[B] are padding and are ignored.  NULL: T = B and
+ *            every sequence gets one token; a length of 0 then marks an unused row, of
+ *            which nothing is written.
+ * seqlens    [B] int32 device array: tokens in each sequence AFTER the write.  The n new
+ *            ones take positions seqlens[b]-n .. seqlens[b]-1.  A length above Lmax or
+ *            below n sets GATTN_DEVICE_BAD_SEQLEN and that sequence is left alone.
+ * T = 0 returns GATTN_OK without launching anything; T * G < 2^31.
+ */
+gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, const int32_t* block_table, int num_pages,
+                                int page_size, int max_pages, const int32_t* seqlens, const int32_t* cu_seqlens,
+                                const void* knorm_w, int T, int B, int G, int d, int rotary_dim, double rope_base,
+                                float eps, int64_t k_tok_stride, int64_t k_head_stride, int64_t v_tok_stride,
+                                int64_t v_head_stride, int dtype, void* stream);
+
+/*
+ * Read cached tokens back: k, v [T,G,d] contiguous, 16-byte aligned, GATTN_BF16 or
+ * GATTN_FP32 (the exact value centre + scale * (code - 8), rounded once).  Rows
+ * [cu_seqlens[b], cu_seqlens[b+1]) receive the tokens starts[b], starts[b]+1, ... of
+ * sequence b (cu_seqlens as for gattn_qcache_write, device memory, NULL: one token
+ * each; starts [B] int32 device array, NULL: zeros).  Rows at or past cu_seqlens[B], and
+ * those of a sequence whose range leaves [0, Lmax) (GATTN_DEVICE_BAD_SEQLEN) or whose
+ * page is not in the pool (GATTN_DEVICE_BAD_PAGE), are left as they were.
+ */
+gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, int num_pages, int page_size,
+                               int max_pages, const int32_t* starts, const int32_t* cu_seqlens, int T, int B, int G,
+                               int d, int dtype, void* k, void* v, void* stream);
+
+/*
+ * One decode step against the 4-bit cache: gattn_decode_paged's mathematics with K and V
+ * as the cache holds them.
+ *
+ * q_new    [B,H,d] bf16 at q_new[b*q_seq_stride + h*q_head_stride + e] (0: contiguous;
+ *          multiples of 16 bytes), e.g. the query halves of a packed [B,H,2d].
+ * gate     as for gattn_decode, at gate[b*gate_seq_stride + h*gate_head_stride (+ e)]
+ *          (0: contiguous).
+ * seqlens  [B] int32 device array, tokens of each sequence INCLUDING the new one, each in
+ *          [0, Lmax].  0 marks an unused row: nothing is appended, and its output is the
+ *          gate applied to the empty sum 0.  A value outside the range sets
+ *          GATTN_DEVICE_BAD_SEQLEN and leaves that row of out unwritten.
+ * k_new, v_new, knorm_w  NULL for no append, else [B,G,d] contiguous and [d] bf16: the
+ *          new token is first written to the cache, as by gattn_qcache_write.
+ * H/G <= 8, B <= 2048; only GATTN_BF16 (implied).
+ * workspace  >= gattn_decode_qcache_workspace_size(B, H, G, d, Lmax) bytes, 256-byte
+ *          aligned; out [B,H*d] bf16, 16-byte aligned.
+ */
+size_t gattn_decode_qcache_workspace_size(int B, int H, int G, int d, int Lmax);
+gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const void* v_new, void* qcache,
+                                 const int32_t* block_table, int num_pages, int page_size, int max_pages,
+                                 const int32_t* seqlens, const void* gate, const void* qnorm_w, const void* knorm_w,
+                                 int B, int H, int G, int d, int rotary_dim, double rope_base, float eps,
+                                 int gate_mode, int64_t q_seq_stride, int64_t q_head_stride, int64_t gate_seq_stride,
+                                 int64_t gate_head_stride, void* workspace, size_t workspace_bytes, void* out,
+                                 void* stream);
+
+/*
  * Read (synchronously on `stream`) and clear the device status word.  Writes the
  * GATTN_DEVICE_* bits seen since the last call to *bits (may be NULL) and returns
  * GATTN_ERR_DEVICE_TIMEOUT if GATTN_DEVICE_TIMEOUT is among them,
