@@ -1,178 +1,715 @@
 // decode_qcache.cu -- one decode step of gated GQA attention against the 4-bit KV
 // cache (format: qcache.cuh).
 //
-// The keys of a sequence are cut into chunks of kChunk; one block per (chunk, KV head,
-// sequence) computes the chunk's partial softmax state (maximum, sum, unnormalised
-// output) for the head's H/G queries, and a second pass merges the chunks and applies
-// the output gate.
+// The step has to read sum(L) * 2 G d * 0.625 bytes of cache, so the design goal is the
+// same as for the bf16 decode -- keep every SM streaming -- but a byte now carries 1.6
+// numbers instead of half a one, and the instructions that unpack them decide how much
+// of the bandwidth is reached.
+//
+//   qdecode_split_kernel  persistent, a few CTAs per SM.  The (sequence, KV head) pairs
+//       are cut into 64-key tiles and the global tile list into equal contiguous ranges,
+//       one per CTA.  A producer warp copies K and V blocks into a ring with 1-D bulk
+//       copies (a tile is four 16-token blocks, contiguous within a page); consumer warp
+//       w owns block w of every tile, so the four keep their own softmax states and meet
+//       only at the end of a piece, where they are merged in shared memory.
+//         S = Q K^T   m16n8k16, fp16.  The H/G queries are the rows.  Codes become fp16
+//             operands without arithmetic: a nibble or-ed into the low mantissa bits of
+//             1024 reads as 1024 + code (or 1024 + 16 code one nibble higher, with q / 16),
+//             and the accumulator starts at minus the constant's share, so it ends at
+//             sum q (code - 8) exactly as if the operand had been code - 8.  Each group's
+//             sum is scaled once per key; the centres enter by one more product,
+//             centre_k . (sum of q over the group), q's sums split into two bf16 parts.
+//         O^T += V^T P^T   m16n8k16, bf16.  The rows are features, so the pairs an operand
+//             register holds are two keys of one feature: two words of neighbouring keys
+//             are interleaved once by halves, and every nibble position of the result is
+//             such a pair.  Code - 8 is exact in bf16; the scales multiply P instead
+//             (they are per key and group), and the centres' part, sum_k p_k centre_k, is
+//             one product for all groups.
+//   qdecode_combine_kernel  merges the partial states of pieces that several CTAs share
+//       and applies the gate; a (sequence, KV head) that one CTA covered is finished by
+//       that CTA.
+#include <cuda_fp16.h>
+
 #include "qcache.cuh"
 
 namespace gattn {
 namespace {
 
-constexpr int kChunk = 256;
+constexpr int BT = 64;   // keys per tile
+constexpr int NCW = 4;   // consumer warps, one per 16-token block of a tile
+constexpr int THREADS = 32 * (NCW + 1);
 
-// The newest query of every head of one KV group, normed and rotated: q[h][e] (fp32).
 template <int D>
-__device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos, float (*q)[D]) {
-    const int r = p.H / p.G, lane = threadIdx.x & 31, nwarp = blockDim.x >> 5;
-    const bf16* w = static_cast<const bf16*>(p.qnorm_w);
-    for (int h = threadIdx.x >> 5; h < r; h += nwarp) {
-        const bf16* row = static_cast<const bf16*>(p.q) + b * p.q_seq_stride + (int64_t)(g * r + h) * p.q_head_stride;
-        float ss = 0.f;
-        for (int e = lane; e < D; e += 32) {
-            const float x = __bfloat162float(row[e]);
-            ss = fmaf(x, x, ss);
-            q[h][e] = x * __bfloat162float(w[e]);
+struct QdCfg {
+    static constexpr int NG = D / kQcGroup;                  // scale groups
+    static constexpr int BLOCK_BYTES = 10 * D;               // one 16-token block
+    static constexpr int TILE_BYTES = 4 * BLOCK_BYTES;       // one plane's share of a tile
+    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;       // K then V
+    static constexpr int CTAS_PER_SM = D == 256 ? 3 : 4;
+    static constexpr int MAX_STAGES = 8;
+    static constexpr int OROW = D + 4;                       // floats per row of the merge buffer (banks)
+    // shared memory behind the ring
+    static constexpr int OFF_QF = 0;                         // uint4 [NG][32] A fragments of the queries
+    static constexpr int OFF_CINIT = OFF_QF + NG * 512;      // float [NG][8] accumulator start
+    static constexpr int OFF_QSUM = OFF_CINIT + NG * 32;     // bf16 [2][8 heads][8 groups], high and low parts
+    static constexpr int OFF_QSC = OFF_QSUM + 256;           // float [8] logit scale of a head
+    static constexpr int OFF_ML = OFF_QSC + 32;              // float [NCW][8][2] the warps' (max, sum)
+    static constexpr int OFF_BAR = OFF_ML + NCW * 64;
+    static constexpr int OFF_MISC = OFF_BAR + 16 * MAX_STAGES;
+    static constexpr int OFF_RED = OFF_MISC + 16;            // int [8] scan scratch
+    static constexpr int OFF_OBUF = OFF_RED + 32;            // float [r][OROW]; the sine table (rd/2 float2) before it
+};
+
+// Bytes of the merge buffer / sine table, and of everything behind the ring.
+template <int D>
+__host__ __device__ int obuf_bytes(int r, int rd) {
+    const int o = r * QdCfg<D>::OROW * 4, t = (rd / 2) * 8;
+    return o > t ? o : t;
+}
+template <int D>
+__host__ __device__ int tail_bytes(int B, int r, int rd) {
+    return QdCfg<D>::OFF_OBUF + obuf_bytes<D>(r, rd) + 4 * (B + 1);
+}
+
+__device__ __forceinline__ int seq_tiles(int L, int Lmax) { return (L >= 1 && L <= Lmax) ? (L + BT - 1) / BT : 0; }
+
+// Exclusive prefix of per-sequence tile counts into pb[0..B]; all threads.
+__device__ void tile_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, int* red) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int carry = 0;
+    for (int base = 0; base < B; base += THREADS) {
+        const int i = base + tid;
+        int v = i < B ? seq_tiles(seqlens[i], Lmax) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += n;
+        }
+        if (lane == 31) red[warp] = v;
+        __syncthreads();
+        int before = carry, total = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) before += red[w];
+            total += red[w];
+        }
+        if (i < B) pb[i + 1] = before + v;
+        __syncthreads();
+        carry += total;
+    }
+    if (tid == 0) pb[0] = 0;
+    __syncthreads();
+}
+
+// Tile u of the global list: sequence b, group g, tile i of its nt.
+struct TileAt {
+    int b, g, i, nt;
+};
+__device__ __forceinline__ TileAt tile_at(int64_t u, const int* pb, int B, int G) {
+    int lo = 0, hi = B - 1;  // largest b with G * pb[b] <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)G * pb[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    TileAt t;
+    t.b = lo;
+    t.nt = pb[lo + 1] - pb[lo];
+    const int rel = (int)(u - (int64_t)G * pb[lo]);
+    t.g = rel / t.nt;
+    t.i = rel % t.nt;
+    return t;
+}
+
+// C[16x8] += A[16x16] * B[16x8], fp16 inputs; rows 8..15 of A are zero.
+__device__ __forceinline__ void mma_f16_top(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) { return __uint_as_float(lds32(a)); }
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
+
+// The gate applied to one output value (e: feature).
+__device__ __forceinline__ float gated(const QcacheDecodeParams& p, int b, int h, int e, float o) {
+    const int layout = gate_layout(p.gate_mode);
+    if (layout == GATTN_GATE_NONE) return o;
+    const bf16* gp = static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride;
+    const float z = __bfloat162float(layout == GATTN_GATE_ELEMENTWISE ? gp[h * p.gate_head_stride + e]
+                                     : layout == GATTN_GATE_HEADWISE  ? gp[h * p.gate_head_stride]
+                                                                      : gp[e]);
+    const float a = gate_act(z, sigmoidf_dev(z), p.gate_mode);
+    return gate_additive(p.gate_mode) ? o + a : o * a;
+}
+
+// The queries of one piece as A fragments (all 128 consumer threads).  A thread takes
+// eight neighbouring features of a head; q' is scaled by a power of two that brings the
+// head's largest |q'| into [0.5, 1), so any norm weights fit fp16, and the power goes
+// into the logit scale.  Two of the four operand registers of a group hold q / 16
+// (the codes they meet sit one nibble higher).
+template <int D>
+__device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos, uint8_t* tail) {
+    using C = QdCfg<D>;
+    constexpr int LPH = D / 8, HPW = 32 / LPH;  // lanes per head, heads per warp and pass
+    const int r = p.H / p.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float2* table = reinterpret_cast<float2*>(tail + C::OFF_OBUF);
+    named_barrier(1, 32 * NCW);  // the previous piece has left the fragments and the merge buffer
+    for (int i = tid; i < (p.rd >> 1); i += 32 * NCW) {
+        float s, c;
+        rope_turn_sincos(p.turns[i], pos, &s, &c);
+        table[i] = make_float2(s, c);
+    }
+    named_barrier(1, 32 * NCW);
+    const int half = p.rd >> 1, u = lane % LPH, e0 = 8 * u;
+    for (int h0 = warp * HPW; h0 < r; h0 += NCW * HPW) {
+        const int h = h0 + lane / LPH;
+        const bool live = h < r;
+        float x[8], w[8], ss = 0.f;
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.q) + b * p.q_seq_stride +
+                                                (int64_t)(g * r + (live ? h : 0)) * p.q_head_stride + e0), x);
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.qnorm_w) + e0), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ss = fmaf(x[i], x[i], ss);
+            w[i] *= x[i];
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float rinv = 1.0f / sqrtf(ss / (float)D + p.eps);
-        __syncwarp();
-        const int half = p.rd >> 1;
-        for (int e = lane; e < half; e += 32) {
-            float s, c;
-            rope_turn_sincos(p.turns[e], pos, &s, &c);
-            const float x0 = q[h][e], x1 = q[h][e + half];
-            q[h][e] = (x0 * c - x1 * s) * rinv;
-            q[h][e + half] = (x1 * c + x0 * s) * rinv;
+        const bool rot = e0 < p.rd, first = e0 < half;
+        const int src = rot ? lane + (first ? half >> 3 : -(half >> 3)) : lane;
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float o = __shfl_sync(0xffffffffu, w[i], src);
+            const float2 sc = rot ? table[(first ? e0 : e0 - half) + i] : make_float2(0.f, 1.f);
+            x[i] = fmaf(w[i], sc.y, o * (first ? -sc.x : sc.x)) * rinv;
+            big = fmaxf(big, fabsf(x[i]));
         }
-        for (int e = p.rd + lane; e < D; e += 32) q[h][e] *= rinv;
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        // 2^-k with big in [2^(k-1), 2^k); 1 for a zero or non-finite row
+        const int ex = (int)((__float_as_uint(big) >> 23) & 255u);
+        const bool plain = ex == 0 || ex == 255;
+        const float down = plain ? 1.f : __uint_as_float((uint32_t)min(max(253 - ex, 1), 254) << 23);
+        const float up = plain ? 1.f : 1.f / down;
+        float cinit = 0.f, qsum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool high = i & 1;  // codes 1, 3, 5, 7 of a word are met as 1024 + 16 code
+            const float y = round_f16(x[i] * down * (high ? 0.0625f : 1.f));
+            x[i] = y;
+            cinit -= (high ? 1152.f : 1032.f) * y;
+            qsum += (high ? 16.f : 1.f) * y;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            cinit += __shfl_xor_sync(0xffffffffu, cinit, o);
+            qsum += __shfl_xor_sync(0xffffffffu, qsum, o);
+        }
+        if (live) {
+            const int grp = u >> 2, t = u & 3;
+            reinterpret_cast<uint4*>(tail + C::OFF_QF)[grp * 32 + h * 4 + t] =
+                make_uint4(pack_f16x2(x[0], x[4]), pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
+            if (t == 0) {
+                reinterpret_cast<float*>(tail + C::OFF_CINIT)[grp * 8 + h] = cinit;
+                bf16* qs = reinterpret_cast<bf16*>(tail + C::OFF_QSUM);
+                const bf16 hi = __float2bfloat16_rn(qsum);
+                qs[h * 8 + grp] = hi;
+                qs[64 + h * 8 + grp] = __float2bfloat16_rn(qsum - __bfloat162float(hi));
+            }
+            if (u == 0) reinterpret_cast<float*>(tail + C::OFF_QSC)[h] = p.scale_log2 * up;
+        }
     }
-    __syncthreads();
-}
-
-__device__ __forceinline__ const uint8_t* key_block(const QcacheDecodeParams& p, int b, int g, int key) {
-    int page = p.block_table[(int64_t)b * p.max_pages + key / p.page_size];
-    if (page < 0 || page >= p.num_pages) {
-        atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
-        page = 0;
-    }
-    return p.cache + qc_block_offset(page, g, key % p.page_size, p.G, p.page_size, p.d);
-}
-
-// value of feature e of row `row` of a block
-__device__ __forceinline__ float qc_value(const uint8_t* block, int row, int e, int d) {
-    const uint8_t byte = block[(e >> 6) * 512 + row * 32 + 4 * ((e & 31) >> 2) + 2 * ((e >> 5) & 1) + ((e & 3) >> 1)];
-    const bf16* par = reinterpret_cast<const bf16*>(block + 8 * d) + (e >> 5) * 16 + row;
-    const int n = (int)((byte >> (4 * (e & 1))) & 15) - 8;
-    return fmaf(__bfloat162float(par[0]), (float)n, __bfloat162float(par[d / 2]));
+    named_barrier(1, 32 * NCW);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kChunk) qdecode_chunk_kernel(const __grid_constant__ QcacheDecodeParams p) {
-    __shared__ float q[8][D];
-    __shared__ float sc[8][kChunk];
-    __shared__ const uint8_t* blocks[kChunk / kQcBlock];
-    const int g = blockIdx.y, b = blockIdx.z, r = p.H / p.G;
-    const int L = p.seqlens[b], k0 = blockIdx.x * kChunk;
-    if (L < 1 || L > p.max_pages * p.page_size || k0 >= L) return;
-    const int n = min(kChunk, L - k0), tid = threadIdx.x;
-    if (tid < kChunk / kQcBlock && tid * kQcBlock < n) blocks[tid] = key_block(p, b, g, k0 + tid * kQcBlock);
-    make_queries<D>(p, b, g, L - 1, q);
-    float acc[8] = {};
-    if (tid < n) {
-        for (int e = 0; e < D; ++e) {
-            const float kv = qc_value(blocks[tid / kQcBlock], tid % kQcBlock, e, D);
-#pragma unroll
-            for (int h = 0; h < 8; ++h)
-                if (h < r) acc[h] = fmaf(q[h][e], kv, acc[h]);
+__global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
+    qdecode_split_kernel(const __grid_constant__ QcacheDecodeParams p, int n_stages, bool after_write) {
+    using C = QdCfg<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    uint8_t* tail = smem + n_stages * C::STAGE_BYTES;
+    const uint32_t stail = sbase + n_stages * C::STAGE_BYTES;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = p.H / p.G, Lmax = p.max_pages * p.page_size;
+    int* pb = reinterpret_cast<int*>(tail + C::OFF_OBUF + obuf_bytes<D>(r, p.rd));
+    const uint32_t bar_full = stail + C::OFF_BAR, bar_empty = bar_full + 8 * C::MAX_STAGES;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
+    pdl_launch_dependents();  // the combine kernel may become resident; it waits for this grid to finish
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < n_stages; ++s) {
+            mbar_init(bar_full + 8 * s, 1);
+            mbar_init(bar_empty + 8 * s, NCW);
         }
+        *abort_flag = 0;
+        fence_mbar_init();
     }
-#pragma unroll
-    for (int h = 0; h < 8; ++h)
-        if (h < r) sc[h][tid] = tid < n ? acc[h] * p.scale_log2 : -INFINITY;
-    __syncthreads();
-    const int64_t nch = gridDim.x;
-    const int lane = tid & 31;
-    for (int h = tid >> 5; h < r; h += kChunk / 32) {
-        float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, sc[h][i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        for (int i = lane; i < n; i += 32) {
-            sc[h][i] = exp2f(sc[h][i] - m);
-            l += sc[h][i];
+    // rows of heads that do not exist stay zero
+    for (int i = threadIdx.x; i < C::OFF_QSC / 4 + 8; i += THREADS) reinterpret_cast<uint32_t*>(tail)[i] = 0u;
+    tile_prefix(p.seqlens, p.B, Lmax, pb, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
+
+    const int64_t T = (int64_t)p.G * pb[p.B];
+    const int64_t u_begin = (int64_t)blockIdx.x * T / gridDim.x;
+    const int64_t u_end = (int64_t)(blockIdx.x + 1) * T / gridDim.x;
+    const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * C::BLOCK_BYTES;
+
+    if (warp == NCW) {
+        // ------------------------------------------------------------ producer (all lanes)
+        if (after_write) {  // the appended rows were written by the kernel before this one
+            pdl_wait_prerequisites();
+            fence_proxy_async_global();
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const int bpp = p.page_size / kQcBlock;
+        const bool whole = p.page_size % BT == 0;  // a tile never leaves its page: one copy a plane
+        int st = 0;
+        uint32_t phase = 1;
+        int64_t u = u_begin;
+        bool ok = true;
+        while (u < u_end && ok) {
+            // lane 4 j + k looks up block k of tile u + j: eight tiles' table entries in one go
+            const int64_t mine = u + (lane >> 2);
+            const uint8_t* src = nullptr;
+            int blocks = 0;
+            if (mine < u_end) {
+                const TileAt t = tile_at(mine, pb, p.B, p.G);
+                blocks = min(4, (p.seqlens[t.b] - t.i * BT + kQcBlock - 1) / kQcBlock);
+                const int blk = t.i * (BT / kQcBlock) + (whole ? 0 : lane & 3);
+                if ((lane & 3) < blocks) {
+                    int page = p.block_table[(int64_t)t.b * p.max_pages + blk / bpp];
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
+                        page = 0;
+                    }
+                    src = p.cache + (((int64_t)page * p.G + t.g) * bpp + blk % bpp) * C::BLOCK_BYTES;
+                }
+            }
+            const int n = (int)min((int64_t)8, u_end - u);
+            for (int j = 0; j < n; ++j, ++u) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * st, phase, abort_flag, p.status) && !*abort_flag);
+                if (!ok) break;
+                const int k = lane - 4 * j;
+                const uint32_t bar = bar_full + 8 * st, dst = sbase + st * C::STAGE_BYTES;
+                if (k == 0) mbar_arrive_expect_tx(bar, 2 * blocks * C::BLOCK_BYTES);
+                __syncwarp();
+                if (k >= 0 && k < (whole ? 1 : blocks)) {
+                    const uint32_t bytes = (whole ? blocks : 1) * C::BLOCK_BYTES;
+                    bulk_load(dst + k * C::BLOCK_BYTES, src, bytes, bar);
+                    bulk_load(dst + C::TILE_BYTES + k * C::BLOCK_BYTES, src + plane, bytes, bar);
+                }
+                if (++st == n_stages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every copy that was sent lands before the block leaves
         if (lane == 0) {
-            float* ps = p.part + (((int64_t)b * p.H + g * r + h) * nch + blockIdx.x) * (D + 2);
-            ps[0] = m;
-            ps[1] = l;
+            const int64_t sent = u - u_begin;
+            for (int64_t j = sent > n_stages ? sent - n_stages : 0; j < sent; ++j)
+                mbar_wait_drain(bar_full + 8 * (int)(j % n_stages), (uint32_t)(j / n_stages) & 1u, p.status);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ consumers
+        const int gid = lane >> 2, t = lane & 3;
+        // V words are read so that the four lanes of a t-quad touch different banks: the upper
+        // two take the pair's second key first, and the interleave undoes it
+        const int kf = 2 * t + (t >> 1), ks = 2 * t + 1 - (t >> 1);
+        const uint32_t sel_lo = t < 2 ? 0x5410u : 0x1054u, sel_hi = t < 2 ? 0x7632u : 0x3276u;
+        constexpr uint32_t kOne16 = 0x64006400u, kOneB = 0x43004300u, kMidB = 0x43084308u;  // 1024 | 128 | 136
+        int st = 0;
+        uint32_t phase = 0;
+        bool dead = false;
+        int64_t u = u_begin;
+        while (u < u_end) {
+            const TileAt at = tile_at(u, pb, p.B, p.G);
+            const int i1 = (int)min((int64_t)at.nt, at.i + (u_end - u));
+            const int L = p.seqlens[at.b];
+            make_queries<D>(p, at.b, at.g, L - 1, tail);
+            const float qsc = lds_f32(stail + C::OFF_QSC + gid * 4);
+            const uint32_t qhi = lds32(stail + C::OFF_QSUM + gid * 16 + t * 4);
+            const uint32_t qlo = lds32(stail + C::OFF_QSUM + 128 + gid * 16 + t * 4);
+            float oacc[2 * C::NG][4], cacc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < 2 * C::NG; ++m) oacc[m][0] = oacc[m][1] = oacc[m][2] = oacc[m][3] = 0.f;
+            float m_run = -INFINITY, l_run = 0.f;
+
+            for (int i = at.i; i < i1; ++i) {
+                if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * st, phase, abort_flag, p.status)))
+                    dead = true;  // keep walking: the block's barriers need every warp
+                const int key0 = i * BT + 16 * warp;
+                if (!dead && key0 < L) {
+                    const uint32_t kb = sbase + st * C::STAGE_BYTES + warp * C::BLOCK_BYTES;
+                    const uint32_t vb = kb + C::TILE_BYTES;
+                    if (key0 + 16 > L) {  // rows past the end may hold anything: no scale, no centre
+                        uint16_t* par = reinterpret_cast<uint16_t*>(smem + st * C::STAGE_BYTES + C::TILE_BYTES +
+                                                                    warp * C::BLOCK_BYTES + 8 * D);
+                        for (int j = lane; j < 2 * C::NG * 16; j += 32)
+                            if (key0 + (j & 15) >= L) par[j] = 0;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    // ---- S = Q K^T, eight keys at a time: lane holds head gid, keys 2t and 2t + 1
+                    float x[2][2];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        float s[4] = {0.f, 0.f, 0.f, 0.f};
+                        uint32_t cp = 0;
+                        if (2 * t < C::NG) {
+                            const uint32_t ca = kb + 9 * D + 2 * t * 32 + (nt * 8 + gid) * 2;
+                            cp = lds16(ca) | (lds16(ca + 32) << 16);
+                        }
+                        mma_bf16_16816(s, qhi, 0u, qlo, 0u, cp, cp);
+#pragma unroll
+                        for (int sl = 0; sl < D / 64; ++sl) {
+                            const uint2 w = lds64(kb + sl * 512 + (nt * 8 + gid) * 32 + t * 8);
+                            uint32_t c[2] = {__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632)};
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const int grp = 2 * sl + hf;
+                                const uint4 qf = lds_v4(stail + C::OFF_QF + grp * 512 + lane * 16);
+                                const float ci = lds_f32(stail + C::OFF_CINIT + grp * 32 + gid * 4);
+                                float a[4] = {ci, ci, 0.f, 0.f};
+                                mma_f16_top(a, qf.x, qf.y, (c[hf] & 0x000F000Fu) | kOne16, (c[hf] & 0x00F000F0u) | kOne16);
+                                c[hf] >>= 8;
+                                mma_f16_top(a, qf.z, qf.w, (c[hf] & 0x000F000Fu) | kOne16, (c[hf] & 0x00F000F0u) | kOne16);
+                                const uint32_t sc = lds32(kb + 8 * D + grp * 32 + nt * 16 + t * 4);
+                                s[0] = fmaf(bf16_lo(sc), a[0], s[0]);
+                                s[1] = fmaf(bf16_hi(sc), a[1], s[1]);
+                            }
+                        }
+                        const int key = key0 + nt * 8 + 2 * t;
+                        x[nt][0] = key < L ? s[0] * qsc : -INFINITY;
+                        x[nt][1] = key + 1 < L ? s[1] * qsc : -INFINITY;
+                    }
+                    // ---- online softmax; the reference moves only when a head's maximum grew by 2^8
+                    float tmax = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+                    tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
+                    tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+                    if (__any_sync(0xffffffffu, tmax > m_run + 8.f)) {
+                        const float m_new = fmaxf(m_run, tmax);
+                        const float alpha = m_run == m_new ? 1.f : ex2_approx(m_run - m_new);
+                        m_run = m_new;
+                        l_run *= alpha;
+                        const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * t);
+                        const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+#pragma unroll
+                        for (int m = 0; m < 2 * C::NG; ++m) {
+                            oacc[m][0] *= a_lo;
+                            oacc[m][1] *= a_hi;
+                            oacc[m][2] *= a_lo;
+                            oacc[m][3] *= a_hi;
+                        }
+                        cacc[0] *= a_lo;
+                        cacc[1] *= a_hi;
+                    }
+                    uint32_t pr[2];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        pr[nt] = pack_bf16x2(ex2_approx(x[nt][0] - m_run), ex2_approx(x[nt][1] - m_run));
+                        l_run += bf16_lo(pr[nt]) + bf16_hi(pr[nt]);  // the sum of the weights as they are used
+                    }
+                    // ---- centres: row g of A is group g
+                    {
+                        const uint32_t ca = vb + 9 * D + gid * 32 + t * 4;
+                        const bool real = gid < C::NG;
+                        mma_bf16_16816(cacc, real ? lds32(ca) : 0u, 0u, real ? lds32(ca + 16) : 0u, 0u, pr[0], pr[1]);
+                    }
+                    // ---- O^T += V^T P^T
+#pragma unroll
+                    for (int sl = 0; sl < D / 64; ++sl) {
+                        const uint32_t va = vb + sl * 512 + gid * 4;
+                        const uint32_t f0 = lds32(va + kf * 32), s0 = lds32(va + ks * 32);
+                        const uint32_t f1 = lds32(va + 256 + kf * 32), s1 = lds32(va + 256 + ks * 32);
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int grp = 2 * sl + hf;
+                            const uint32_t sel = hf ? sel_hi : sel_lo;
+                            const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
+                            const uint32_t sa = vb + 8 * D + grp * 32 + t * 4;
+                            const uint32_t p0 = mul_bf16x2(pr[0], lds32(sa)), p1 = mul_bf16x2(pr[1], lds32(sa + 16));
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                uint32_t a[4];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int sh = 4 * (2 * m + k);
+                                    a[k] = sub_bf16x2(((w0 >> sh) & 0x000F000Fu) | kOneB, kMidB);
+                                    a[2 + k] = sub_bf16x2(((w1 >> sh) & 0x000F000Fu) | kOneB, kMidB);
+                                }
+                                mma_bf16_16816(oacc[2 * grp + m], a[0], a[1], a[2], a[3], p0, p1);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_empty + 8 * st);
+                if (++st == n_stages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+
+            // -------- end of the piece: merge the four warps, then finish or hand over
+            l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+            l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+            float* ml = reinterpret_cast<float*>(tail + C::OFF_ML);
+            float* obuf = reinterpret_cast<float*>(tail + C::OFF_OBUF);
+            if (t == 0) {
+                ml[(warp * 8 + gid) * 2] = m_run;
+                ml[(warp * 8 + gid) * 2 + 1] = l_run;
+            }
+            named_barrier(1, 32 * NCW);
+            // weight of this warp's state for the lane's two heads
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = -INFINITY;
+                for (int w = 0; w < NCW; ++w) mx = fmaxf(mx, ml[(w * 8 + 2 * t + e) * 2]);
+                const float mine = ml[(warp * 8 + 2 * t + e) * 2];
+                f[e] = mine == -INFINITY ? 0.f : ex2_approx(mine - mx);
+            }
+            for (int w = 0; w < NCW; ++w) {
+                if (w == warp) {
+#pragma unroll
+                    for (int grp = 0; grp < C::NG; ++grp) {
+                        const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * grp + t);
+                        const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * grp + t);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int h = 2 * t + e;
+                            const float c = e ? c1 : c0;
+                            float4* at4 = reinterpret_cast<float4*>(obuf + h * C::OROW + grp * 32 + gid * 4);
+                            if (h < r) {
+                                float4 o = w ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (f[e] != 0.f) {
+                                    o.x = fmaf(f[e], oacc[2 * grp][e] + c, o.x);
+                                    o.y = fmaf(f[e], oacc[2 * grp][2 + e] + c, o.y);
+                                    o.z = fmaf(f[e], oacc[2 * grp + 1][e] + c, o.z);
+                                    o.w = fmaf(f[e], oacc[2 * grp + 1][2 + e] + c, o.w);
+                                }
+                                *at4 = o;
+                            }
+                        }
+                    }
+                }
+                named_barrier(1, 32 * NCW);
+            }
+            const bool alone = at.i == 0 && i1 == at.nt;
+            const int64_t seg = (int64_t)at.b * p.G + at.g;
+            float* ps = p.part + ((int64_t)blockIdx.x + seg) * (int64_t)(2 * r + r * D);
+            for (int h = 0; h < r; ++h) {
+                float mx = -INFINITY, l = 0.f;
+                for (int w = 0; w < NCW; ++w) mx = fmaxf(mx, ml[(w * 8 + h) * 2]);
+                for (int w = 0; w < NCW; ++w) {
+                    const float mw = ml[(w * 8 + h) * 2];
+                    l += mw == -INFINITY ? 0.f : ex2_approx(mw - mx) * ml[(w * 8 + h) * 2 + 1];
+                }
+                for (int e = threadIdx.x; e < D; e += 32 * NCW) {
+                    const float o = obuf[h * C::OROW + e];
+                    if (alone) {
+                        static_cast<bf16*>(p.out)[((int64_t)at.b * p.H + at.g * r + h) * D + e] =
+                            __float2bfloat16_rn(gated(p, at.b, at.g * r + h, e, o / l));
+                    } else {
+                        ps[2 * r + h * D + e] = o;
+                    }
+                }
+                if (!alone && threadIdx.x == 0) {
+                    ps[h] = mx;
+                    ps[r + h] = l;
+                }
+            }
+            u += i1 - at.i;
         }
     }
     __syncthreads();
-    const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * qc_block_bytes(D);
-    for (int e = tid; e < D; e += kChunk) {
-        float o[8] = {};
-        for (int i = 0; i < n; ++i) {
-            const float v = qc_value(blocks[i / kQcBlock] + plane, i % kQcBlock, e, D);
-#pragma unroll
-            for (int h = 0; h < 8; ++h)
-                if (h < r) o[h] = fmaf(sc[h][i], v, o[h]);
-        }
-        for (int h = 0; h < r; ++h)
-            p.part[(((int64_t)b * p.H + g * r + h) * nch + blockIdx.x) * (D + 2) + 2 + e] = o[h];
-    }
 }
 
-// Merge the chunks of one (sequence, head) and apply the gate; one thread per feature.
-__global__ void qdecode_combine_kernel(const __grid_constant__ QcacheDecodeParams p, int nch) {
-    const int h = blockIdx.x, b = blockIdx.y, e = threadIdx.x, d = p.d;
-    const int L = p.seqlens[b];
-    if (L < 0 || L > p.max_pages * p.page_size) {
-        if (e == 0 && h == 0) atomicOr(p.status, GATTN_DEVICE_BAD_SEQLEN);
+// Merge the partial states of one (sequence, KV head) that several CTAs share and apply
+// the gate: warp (part, h) sums every n_parts-th state of head h, lane l owning D / 32
+// features, and the parts meet in shared memory.  A sequence of length 0 gets the gate of
+// an empty sum.
+template <int D>
+__global__ void __launch_bounds__(256) qdecode_combine_kernel(const __grid_constant__ QcacheDecodeParams p, int n_ctas) {
+    constexpr int DPL = D / 32, CH = 4;
+    __shared__ float sm[8][2], so[8][D];
+    const int b = blockIdx.x / p.G, g = blockIdx.x % p.G, r = p.H / p.G, Lmax = p.max_pages * p.page_size;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int L = p.seqlens[b], nt = seq_tiles(L, Lmax);
+    // every block waits for the split kernel before it leaves: this grid's end then means both
+    if (L == 0) {
+        pdl_wait_prerequisites();
+        for (int i = threadIdx.x; i < r * D; i += 256)
+            static_cast<bf16*>(p.out)[((int64_t)b * p.H + g * r) * D + i] =
+                __float2bfloat16_rn(gated(p, b, g * r + i / D, i % D, 0.f));
         return;
     }
-    const int n = (L + kChunk - 1) / kChunk;
-    const float* ps = p.part + ((int64_t)b * p.H + h) * nch * (d + 2);
-    float m = -INFINITY, den = 0.f, num = 0.f;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, ps[(int64_t)i * (d + 2)]);
-    for (int i = 0; i < n; ++i) {
-        const float* s = ps + (int64_t)i * (d + 2);
-        const float w = exp2f(s[0] - m);
-        den = fmaf(w, s[1], den);
-        num = fmaf(w, s[2 + e], num);
+    if (nt == 0) {
+        pdl_wait_prerequisites();
+        if (threadIdx.x == 0 && g == 0) atomicOr(p.status, GATTN_DEVICE_BAD_SEQLEN);
+        return;
     }
-    float o = n ? num / den : 0.f;  // no key: the empty sum
-    const int layout = gate_layout(p.gate_mode);
-    if (layout != GATTN_GATE_NONE) {
-        const bf16* gp = static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride;
-        const float z = __bfloat162float(layout == GATTN_GATE_ELEMENTWISE ? gp[h * p.gate_head_stride + e]
-                                         : layout == GATTN_GATE_HEADWISE  ? gp[h * p.gate_head_stride]
-                                                                          : gp[e]);
-        const float a = gate_act(z, sigmoidf_dev(z), p.gate_mode);
-        o = gate_additive(p.gate_mode) ? o + a : o * a;
+    int before = 0, total = 0;  // tiles ahead of this sequence, and of all
+    for (int i = lane; i < p.B; i += 32) {
+        const int n = seq_tiles(p.seqlens[i], Lmax);
+        total += n;
+        if (i < b) before += n;
     }
-    static_cast<bf16*>(p.out)[((int64_t)b * p.H + h) * d + e] = __float2bfloat16_rn(o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    const int64_t T = (int64_t)p.G * total, N = n_ctas;
+    const int64_t u0 = (int64_t)p.G * before + (int64_t)g * nt, u1 = u0 + nt - 1;
+    // CTA c holds tiles [c T / N, (c + 1) T / N): the one that holds tile x
+    const int64_t c0 = ((u0 + 1) * N - 1) / T, c1 = ((u1 + 1) * N - 1) / T;
+    const int n_parts = 8 / r, h = warp % r, part = warp / r, stride = 2 * r + r * D;
+    const float* part0 = p.part + (c0 + (int64_t)b * p.G + g) * (int64_t)stride;
+    const int n_slots = (int)(c1 - c0) + 1;
+
+    pdl_wait_prerequisites();  // everything above reads only the inputs
+    if (c0 == c1) return;      // one CTA covered and finished it
+    float m_run = -INFINITY, den = 0.f, num[DPL];
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) num[k] = 0.f;
+    if (part < n_parts) {
+        for (int s0 = part; s0 < n_slots; s0 += CH * n_parts) {
+            float ms[CH], ls[CH], os[CH][DPL];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const int s = s0 + j * n_parts;
+                // fewer tiles than CTAs: a CTA between two that hold tiles may hold none
+                const bool live = s < n_slots && (c0 + s) * T / N < (c0 + s + 1) * T / N;
+                const float* ps = part0 + (int64_t)(live ? s : 0) * stride;
+                ms[j] = live ? ps[h] : -INFINITY;
+                ls[j] = live ? ps[r + h] : 0.f;
+#pragma unroll
+                for (int k = 0; k < DPL; ++k) os[j][k] = live ? ps[2 * r + h * D + lane + 32 * k] : 0.f;
+            }
+            float mx = m_run;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) mx = fmaxf(mx, ms[j]);
+            const float keep = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
+            den *= keep;
+#pragma unroll
+            for (int k = 0; k < DPL; ++k) num[k] *= keep;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const float w = ms[j] == -INFINITY ? 0.f : ex2_approx(ms[j] - mx);
+                if (w == 0.f) continue;
+                den = fmaf(w, ls[j], den);
+#pragma unroll
+                for (int k = 0; k < DPL; ++k) num[k] = fmaf(w, os[j][k], num[k]);
+            }
+            m_run = mx;
+        }
+        if (lane == 0) {
+            sm[warp][0] = m_run;
+            sm[warp][1] = den;
+        }
+#pragma unroll
+        for (int k = 0; k < DPL; ++k) so[warp][lane + 32 * k] = num[k];
+    }
+    __syncthreads();
+    if (part != 0) return;
+    float mx = -INFINITY;
+    for (int q = 0; q < n_parts; ++q) mx = fmaxf(mx, sm[q * r + h][0]);
+    den = 0.f;
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) num[k] = 0.f;
+    for (int q = 0; q < n_parts; ++q) {
+        const float mq = sm[q * r + h][0], w = mq == -INFINITY ? 0.f : ex2_approx(mq - mx);
+        if (w == 0.f) continue;
+        den = fmaf(w, sm[q * r + h][1], den);
+#pragma unroll
+        for (int k = 0; k < DPL; ++k) num[k] = fmaf(w, so[q * r + h][lane + 32 * k], num[k]);
+    }
+    bf16* out = static_cast<bf16*>(p.out) + ((int64_t)b * p.H + g * r + h) * D;
+#pragma unroll
+    for (int k = 0; k < DPL; ++k) {
+        const int e = lane + 32 * k;
+        out[e] = __float2bfloat16_rn(gated(p, b, g * r + h, e, num[k] / den));
+    }
 }
 
 template <int D>
-cudaError_t launch_d(const QcacheDecodeParams& p, cudaStream_t stream, cudaEvent_t ev_start, cudaEvent_t ev_stop) {
-    const int nch = (p.max_pages * p.page_size + kChunk - 1) / kChunk;
+cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t stream, cudaEvent_t ev_start,
+                     cudaEvent_t ev_stop) {
+    using C = QdCfg<D>;
+    const int n_ctas = C::CTAS_PER_SM * p.n_sms;
+    // ring depth: what an SM's 228 KB (1 KB of it reserved per CTA) leave for each CTA
+    const int tail = tail_bytes<D>(p.B, p.H / p.G, p.rd);
+    int stages = ((228 * 1024) / C::CTAS_PER_SM - 1024 - tail) / C::STAGE_BYTES;
+    stages = stages < 2 ? 2 : stages > C::MAX_STAGES ? C::MAX_STAGES : stages;
+    cudaError_t e = set_smem_once(reinterpret_cast<const void*>(qdecode_split_kernel<D>), 227 * 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)n_ctas);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = (size_t)(stages * C::STAGE_BYTES + tail);
+    cfg.numAttrs = after_write ? 1 : 0;
     if (ev_start) cudaEventRecord(ev_start, stream);
-    qdecode_chunk_kernel<D><<<dim3(nch, p.G, p.B), kChunk, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, qdecode_split_kernel<D>, p, stages, after_write);
     if (ev_stop) cudaEventRecord(ev_stop, stream);
     if (e != cudaSuccess) return e;
-    qdecode_combine_kernel<<<dim3(p.H, p.B), D, 0, stream>>>(p, nch);
-    return cudaGetLastError();
+    cfg.gridDim = dim3((unsigned)(p.B * p.G));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qdecode_combine_kernel<D>, p, n_ctas);
 }
 
 }  // namespace
 
-size_t qcache_decode_workspace(int B, int H, int G, int d, int Lmax, int n_sms) {
-    (void)G, (void)n_sms;
-    return (size_t)B * H * (((size_t)Lmax + kChunk - 1) / kChunk) * (d + 2) * sizeof(float);
+size_t qcache_decode_workspace(int B, int H, int G, int d, int n_sms) {
+    const int per_sm = d == 256 ? QdCfg<256>::CTAS_PER_SM : QdCfg<64>::CTAS_PER_SM;
+    const int r = H / G;
+    return ((size_t)per_sm * n_sms + (size_t)B * G) * (size_t)(2 * r + r * d) * sizeof(float);
 }
 
-cudaError_t launch_qcache_decode(const QcacheDecodeParams& p, cudaStream_t stream, cudaEvent_t ev_start,
-                                 cudaEvent_t ev_stop) {
+cudaError_t launch_qcache_decode(const QcacheDecodeParams& p, bool after_write, cudaStream_t stream,
+                                 cudaEvent_t ev_start, cudaEvent_t ev_stop) {
     switch (p.d) {
-        case 64: return launch_d<64>(p, stream, ev_start, ev_stop);
-        case 128: return launch_d<128>(p, stream, ev_start, ev_stop);
-        case 256: return launch_d<256>(p, stream, ev_start, ev_stop);
+        case 64: return launch_d<64>(p, after_write, stream, ev_start, ev_stop);
+        case 128: return launch_d<128>(p, after_write, stream, ev_start, ev_stop);
+        case 256: return launch_d<256>(p, after_write, stream, ev_start, ev_stop);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -188,9 +188,10 @@ struct QcacheDecodeParams {
 };
 cudaError_t launch_qcache_write(const QcacheWriteParams& p, bool fp32, cudaStream_t stream);
 cudaError_t launch_qcache_read(const QcacheReadParams& p, bool fp32, cudaStream_t stream);
-size_t qcache_decode_workspace(int B, int H, int G, int d, int Lmax, int n_sms);
-cudaError_t launch_qcache_decode(const QcacheDecodeParams& p, cudaStream_t stream, cudaEvent_t ev_start,
-                                 cudaEvent_t ev_stop);
+size_t qcache_decode_workspace(int B, int H, int G, int d, int n_sms);
+// after_write: the kernel ahead in the stream is this step's launch_qcache_write
+cudaError_t launch_qcache_decode(const QcacheDecodeParams& p, bool after_write, cudaStream_t stream,
+                                 cudaEvent_t ev_start, cudaEvent_t ev_stop);
 
 // Shared by the entry points' translation units (defined in api.cu).
 unsigned int* device_status_word();  // address of the status word on the current device, NULL on failure

@@ -151,7 +151,7 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
 size_t gattn_decode_qcache_workspace_size(int B, int H, int G, int d, int Lmax) {
     if (B < 1 || H < 1 || G < 1 || d < 1 || Lmax < 1 || H % G != 0) return 0;
     const int n = device_sm_count();
-    return n > 0 ? round_up(qcache_decode_workspace(B, H, G, d, Lmax, n), 256) : 0;
+    return n > 0 ? round_up(qcache_decode_workspace(B, H, G, d, n), 256) : 0;
 }
 
 gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const void* v_new, void* qcache,
@@ -221,7 +221,7 @@ gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const voi
     fill_turns(p.turns, rotary_dim, rope_base);
     cudaEvent_t ev_start, ev_stop;
     profile_events(&ev_start, &ev_stop);
-    return launch_qcache_decode(p, stream, ev_start, ev_stop) == cudaSuccess ? GATTN_OK : GATTN_ERR_CUDA;
+    return launch_qcache_decode(p, append, stream, ev_start, ev_stop) == cudaSuccess ? GATTN_OK : GATTN_ERR_CUDA;
 }
 
 }  // extern "C"
