@@ -6,19 +6,22 @@
 // numbers instead of half a one, and the instructions that unpack them decide how much
 // of the bandwidth is reached.
 //
-//   qdecode_split_kernel  persistent, a few CTAs per SM.  The (sequence, KV head) pairs
-//       are cut into 64-key tiles and the global tile list into equal contiguous ranges,
-//       one per CTA.  A producer warp copies K and V blocks into a ring with 1-D bulk
-//       copies (a tile is four 16-token blocks, contiguous within a page); consumer warp
-//       w owns block w of every tile, so the four keep their own softmax states and meet
-//       only at the end of a piece, where they are merged in shared memory.
-//         S = Q K^T   m16n8k16, fp16.  The H/G queries are the rows.  Codes become fp16
-//             operands without arithmetic: a nibble or-ed into the low mantissa bits of
-//             1024 reads as 1024 + code (or 1024 + 16 code one nibble higher, with q / 16),
-//             and the accumulator starts at minus the constant's share, so it ends at
-//             sum q (code - 8) exactly as if the operand had been code - 8.  Each group's
-//             sum is scaled once per key; the centres enter by one more product,
-//             centre_k . (sum of q over the group), q's sums split into two bf16 parts.
+//   qdecode_split_kernel  persistent, a few CTAs of four warps per SM.  The (sequence, KV
+//       head) pairs are cut into 64-key tiles and the global tile list into equal
+//       contiguous ranges, one per CTA.  Warp w owns 16-token block w of every tile: it
+//       copies the block's K and V bytes into a ring of its own with two bulk copies, a
+//       few tiles ahead, and keeps its own softmax state, so the warps meet only at the
+//       end of a piece, where they are merged in shared memory.  (A producer warp for the
+//       four cost a fifth warp's registers, which the accumulators need: 128 a thread
+//       spilled, and 64 sequences of 16k-32k tokens took 432 us.)
+//         S^T = K Q^T   m16n8k16, fp16: sixteen keys by the H/G <= 8 queries.  Codes become
+//             fp16 operands without arithmetic: a nibble or-ed into the low mantissa bits
+//             of 1024 reads as 1024 + code (or 1024 + 16 code one nibble higher, with
+//             q / 16), and the accumulator starts at minus the constant's share, so it ends
+//             at sum q (code - 8) as if the operand had been code - 8.  Each group's sum is
+//             scaled once per key; the centres enter by one more product, centre_k . (sum
+//             of q over the group), q's sums split into two bf16 parts.  The weights turn
+//             into the next product's operand by a register transpose (movmatrix).
 //         O^T += V^T P^T   m16n8k16, bf16.  The rows are features, so the pairs an operand
 //             register holds are two keys of one feature: two words of neighbouring keys
 //             are interleaved once by halves, and every nibble position of the result is
@@ -35,32 +38,31 @@
 namespace gattn {
 namespace {
 
-constexpr int BT = 64;   // keys per tile
-constexpr int NCW = 4;   // consumer warps, one per 16-token block of a tile
-constexpr int THREADS = 32 * (NCW + 1);
+constexpr int BT = 64;  // keys per tile
+constexpr int NW = 4;   // warps, one per 16-token block of a tile
+constexpr int THREADS = 32 * NW;
 
 template <int D>
 struct QdCfg {
-    static constexpr int NG = D / kQcGroup;                  // scale groups
-    static constexpr int BLOCK_BYTES = 10 * D;               // one 16-token block
-    static constexpr int TILE_BYTES = 4 * BLOCK_BYTES;       // one plane's share of a tile
-    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;       // K then V
+    static constexpr int NG = D / kQcGroup;             // scale groups
+    static constexpr int BLOCK_BYTES = 10 * D;          // one 16-token block
+    static constexpr int STAGE_BYTES = 2 * BLOCK_BYTES; // a warp's K and V block
     static constexpr int CTAS_PER_SM = D == 256 ? 3 : 4;
-    static constexpr int MAX_STAGES = 8;
-    static constexpr int OROW = D + 4;                       // floats per row of the merge buffer (banks)
-    // shared memory behind the ring
-    static constexpr int OFF_QF = 0;                         // uint4 [NG][32] A fragments of the queries
-    static constexpr int OFF_CINIT = OFF_QF + NG * 512;      // float [NG][8] accumulator start
-    static constexpr int OFF_QSUM = OFF_CINIT + NG * 32;     // bf16 [2][8 heads][8 groups], high and low parts
+    static constexpr int MAX_STAGES = 8;                // per warp
+    static constexpr int OROW = D + 4;                  // floats per row of the merge buffer (banks)
+    // shared memory: the warps' rings (NW * stages), then
+    static constexpr int OFF_QF = 0;                         // uint4 [NG][32] B fragments of the queries
+    static constexpr int OFF_CINIT = OFF_QF + NG * 512;      // float [NG][4][4] accumulator start of heads 2t, 2t+1, twice
+    static constexpr int OFF_QSUM = OFF_CINIT + NG * 64;     // bf16 [2][8 heads][8 groups], high and low parts
     static constexpr int OFF_QSC = OFF_QSUM + 256;           // float [8] logit scale of a head
-    static constexpr int OFF_ML = OFF_QSC + 32;              // float [NCW][8][2] the warps' (max, sum)
-    static constexpr int OFF_BAR = OFF_ML + NCW * 64;
-    static constexpr int OFF_MISC = OFF_BAR + 16 * MAX_STAGES;
-    static constexpr int OFF_RED = OFF_MISC + 16;            // int [8] scan scratch
-    static constexpr int OFF_OBUF = OFF_RED + 32;            // float [r][OROW]; the sine table (rd/2 float2) before it
+    static constexpr int OFF_ML = OFF_QSC + 32;              // float [NW][8][2] the warps' (max, sum)
+    static constexpr int OFF_BAR = OFF_ML + NW * 64;         // mbarrier [NW][MAX_STAGES]
+    static constexpr int OFF_MISC = OFF_BAR + NW * 8 * MAX_STAGES;
+    static constexpr int OFF_RED = OFF_MISC + 16;            // int [NW] scan scratch
+    static constexpr int OFF_OBUF = OFF_RED + 16;            // float [r][OROW]; the sine table (rd/2 float2) before it
 };
 
-// Bytes of the merge buffer / sine table, and of everything behind the ring.
+// Bytes of the merge buffer / sine table, and of everything behind the rings.
 template <int D>
 __host__ __device__ int obuf_bytes(int r, int rd) {
     const int o = r * QdCfg<D>::OROW * 4, t = (rd / 2) * 8;
@@ -88,7 +90,7 @@ __device__ void tile_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, in
         if (lane == 31) red[warp] = v;
         __syncthreads();
         int before = carry, total = 0;
-        for (int w = 0; w < THREADS / 32; ++w) {
+        for (int w = 0; w < NW; ++w) {
             if (w < warp) before += red[w];
             total += red[w];
         }
@@ -119,29 +121,35 @@ __device__ __forceinline__ TileAt tile_at(int64_t u, const int* pb, int B, int G
     return t;
 }
 
-// C[16x8] += A[16x16] * B[16x8], fp16 inputs; rows 8..15 of A are zero.
-__device__ __forceinline__ void mma_f16_top(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1));
+// D[16x8] = A[16x16] * B[16x8] + C, fp16 inputs.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
+// Transpose of an 8x8 matrix of 16-bit elements spread over the warp, two a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
+// (x & MASK) | bits in one instruction; `bits` has to come from a register (opaque below),
+// since an instruction takes one immediate.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(MASK), "r"(bits));
+    return d;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm volatile("" : "+r"(x));
+    return x;
 }
-__device__ __forceinline__ float lds_f32(uint32_t a) { return __uint_as_float(lds32(a)); }
+template <typename T>
+__device__ __forceinline__ T ld(const uint8_t* p) {
+    return *reinterpret_cast<const T*>(p);
+}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("sub.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -170,8 +178,8 @@ __device__ __forceinline__ float gated(const QcacheDecodeParams& p, int b, int h
     return gate_additive(p.gate_mode) ? o + a : o * a;
 }
 
-// The queries of one piece as A fragments (all 128 consumer threads).  A thread takes
-// eight neighbouring features of a head; q' is scaled by a power of two that brings the
+// The queries of one piece as B fragments (all threads).  A thread takes eight
+// neighbouring features of a head; q' is scaled by a power of two that brings the
 // head's largest |q'| into [0.5, 1), so any norm weights fit fp16, and the power goes
 // into the logit scale.  Two of the four operand registers of a group hold q / 16
 // (the codes they meet sit one nibble higher).
@@ -181,15 +189,15 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
     constexpr int LPH = D / 8, HPW = 32 / LPH;  // lanes per head, heads per warp and pass
     const int r = p.H / p.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float2* table = reinterpret_cast<float2*>(tail + C::OFF_OBUF);
-    named_barrier(1, 32 * NCW);  // the previous piece has left the fragments and the merge buffer
-    for (int i = tid; i < (p.rd >> 1); i += 32 * NCW) {
+    __syncthreads();  // the previous piece has left the fragments and the merge buffer
+    for (int i = tid; i < (p.rd >> 1); i += THREADS) {
         float s, c;
         rope_turn_sincos(p.turns[i], pos, &s, &c);
         table[i] = make_float2(s, c);
     }
-    named_barrier(1, 32 * NCW);
+    __syncthreads();
     const int half = p.rd >> 1, u = lane % LPH, e0 = 8 * u;
-    for (int h0 = warp * HPW; h0 < r; h0 += NCW * HPW) {
+    for (int h0 = warp * HPW; h0 < r; h0 += NW * HPW) {
         const int h = h0 + lane / LPH;
         const bool live = h < r;
         float x[8], w[8], ss = 0.f;
@@ -240,7 +248,8 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
             reinterpret_cast<uint4*>(tail + C::OFF_QF)[grp * 32 + h * 4 + t] =
                 make_uint4(pack_f16x2(x[0], x[4]), pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
             if (t == 0) {
-                reinterpret_cast<float*>(tail + C::OFF_CINIT)[grp * 8 + h] = cinit;
+                float* ci = reinterpret_cast<float*>(tail + C::OFF_CINIT) + (grp * 4 + (h >> 1)) * 4 + (h & 1);
+                ci[0] = ci[2] = cinit;
                 bf16* qs = reinterpret_cast<bf16*>(tail + C::OFF_QSUM);
                 const bf16 hi = __float2bfloat16_rn(qsum);
                 qs[h * 8 + grp] = hi;
@@ -249,7 +258,7 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
             if (u == 0) reinterpret_cast<float*>(tail + C::OFF_QSC)[h] = p.scale_log2 * up;
         }
     }
-    named_barrier(1, 32 * NCW);
+    __syncthreads();
 }
 
 template <int D>
@@ -257,303 +266,316 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     qdecode_split_kernel(const __grid_constant__ QcacheDecodeParams p, int n_stages, bool after_write) {
     using C = QdCfg<D>;
     extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t sbase = smem_u32(smem);
-    uint8_t* tail = smem + n_stages * C::STAGE_BYTES;
-    const uint32_t stail = sbase + n_stages * C::STAGE_BYTES;
+    uint8_t* tail = smem + NW * n_stages * C::STAGE_BYTES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = p.H / p.G, Lmax = p.max_pages * p.page_size;
     int* pb = reinterpret_cast<int*>(tail + C::OFF_OBUF + obuf_bytes<D>(r, p.rd));
-    const uint32_t bar_full = stail + C::OFF_BAR, bar_empty = bar_full + 8 * C::MAX_STAGES;
+    uint8_t* ring = smem + warp * n_stages * C::STAGE_BYTES;
+    const uint32_t bars = smem_u32(tail + C::OFF_BAR) + warp * 8 * C::MAX_STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
     pdl_launch_dependents();  // the combine kernel may become resident; it waits for this grid to finish
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < n_stages; ++s) {
-            mbar_init(bar_full + 8 * s, 1);
-            mbar_init(bar_empty + 8 * s, NCW);
-        }
-        *abort_flag = 0;
+    if (lane == 0) {
+        for (int s = 0; s < n_stages; ++s) mbar_init(bars + 8 * s, 1);
         fence_mbar_init();
     }
+    if (threadIdx.x == 0) *abort_flag = 0;
     // rows of heads that do not exist stay zero
-    for (int i = threadIdx.x; i < C::OFF_QSC / 4 + 8; i += THREADS) reinterpret_cast<uint32_t*>(tail)[i] = 0u;
+    for (int i = threadIdx.x; i < C::OFF_ML / 4; i += THREADS) reinterpret_cast<uint32_t*>(tail)[i] = 0u;
     tile_prefix(p.seqlens, p.B, Lmax, pb, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
 
     const int64_t T = (int64_t)p.G * pb[p.B];
     const int64_t u_begin = (int64_t)blockIdx.x * T / gridDim.x;
     const int64_t u_end = (int64_t)(blockIdx.x + 1) * T / gridDim.x;
     const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * C::BLOCK_BYTES;
+    const int bpp = p.page_size / kQcBlock;
+    if (after_write) {  // the appended rows were written by the kernel before this one
+        pdl_wait_prerequisites();
+        fence_proxy_async_global();
+    }
 
-    if (warp == NCW) {
-        // ------------------------------------------------------------ producer (all lanes)
-        if (after_write) {  // the appended rows were written by the kernel before this one
-            pdl_wait_prerequisites();
-            fence_proxy_async_global();
-        }
-        const int bpp = p.page_size / kQcBlock;
-        const bool whole = p.page_size % BT == 0;  // a tile never leaves its page: one copy a plane
-        int st = 0;
-        uint32_t phase = 1;
-        int64_t u = u_begin;
-        bool ok = true;
-        while (u < u_end && ok) {
-            // lane 4 j + k looks up block k of tile u + j: eight tiles' table entries in one go
-            const int64_t mine = u + (lane >> 2);
-            const uint8_t* src = nullptr;
-            int blocks = 0;
-            if (mine < u_end) {
-                const TileAt t = tile_at(mine, pb, p.B, p.G);
-                blocks = min(4, (p.seqlens[t.b] - t.i * BT + kQcBlock - 1) / kQcBlock);
-                const int blk = t.i * (BT / kQcBlock) + (whole ? 0 : lane & 3);
-                if ((lane & 3) < blocks) {
+    // ---- the warp's copies run n_stages tiles ahead.  Lane j holds the address of the
+    // warp's block of tile batch + j (0: past the sequence's end), 32 table entries a time.
+    int64_t batch = u_begin, sent = u_begin;
+    uint64_t src = 0;
+    uint32_t pending = 0, phases = 0;  // per stage: a copy is under way; parity of its barrier
+    int s_send = 0;
+    auto send = [&]() {  // all lanes; tile `sent` into stage s_send
+        if (sent >= u_end) return;
+        if (sent == u_begin || sent == batch + 32) {
+            batch = sent;
+            src = 0;
+            if (batch + lane < u_end) {
+                const TileAt t = tile_at(batch + lane, pb, p.B, p.G);
+                const int blk = t.i * (BT / kQcBlock) + warp;
+                if (blk * kQcBlock < p.seqlens[t.b]) {
                     int page = p.block_table[(int64_t)t.b * p.max_pages + blk / bpp];
                     if (page < 0 || page >= p.num_pages) {
                         atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
                         page = 0;
                     }
-                    src = p.cache + (((int64_t)page * p.G + t.g) * bpp + blk % bpp) * C::BLOCK_BYTES;
-                }
-            }
-            const int n = (int)min((int64_t)8, u_end - u);
-            for (int j = 0; j < n; ++j, ++u) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar_empty + 8 * st, phase, abort_flag, p.status) && !*abort_flag);
-                if (!ok) break;
-                const int k = lane - 4 * j;
-                const uint32_t bar = bar_full + 8 * st, dst = sbase + st * C::STAGE_BYTES;
-                if (k == 0) mbar_arrive_expect_tx(bar, 2 * blocks * C::BLOCK_BYTES);
-                __syncwarp();
-                if (k >= 0 && k < (whole ? 1 : blocks)) {
-                    const uint32_t bytes = (whole ? blocks : 1) * C::BLOCK_BYTES;
-                    bulk_load(dst + k * C::BLOCK_BYTES, src, bytes, bar);
-                    bulk_load(dst + C::TILE_BYTES + k * C::BLOCK_BYTES, src + plane, bytes, bar);
-                }
-                if (++st == n_stages) {
-                    st = 0;
-                    phase ^= 1u;
+                    src = reinterpret_cast<uint64_t>(p.cache + (((int64_t)page * p.G + t.g) * bpp + blk % bpp) * C::BLOCK_BYTES);
                 }
             }
         }
-        // every copy that was sent lands before the block leaves
-        if (lane == 0) {
-            const int64_t sent = u - u_begin;
-            for (int64_t j = sent > n_stages ? sent - n_stages : 0; j < sent; ++j)
-                mbar_wait_drain(bar_full + 8 * (int)(j % n_stages), (uint32_t)(j / n_stages) & 1u, p.status);
+        const uint64_t a = __shfl_sync(0xffffffffu, src, (int)(sent - batch));
+        if (a) {
+            if (lane == 0) {
+                const uint32_t bar = bars + 8 * s_send, dst = smem_u32(ring + s_send * C::STAGE_BYTES);
+                mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+                bulk_load(dst, reinterpret_cast<const uint8_t*>(a), C::BLOCK_BYTES, bar);
+                bulk_load(dst + C::BLOCK_BYTES, reinterpret_cast<const uint8_t*>(a) + plane, C::BLOCK_BYTES, bar);
+            }
+            pending |= 1u << s_send;
         }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------------ consumers
-        const int gid = lane >> 2, t = lane & 3;
-        // V words are read so that the four lanes of a t-quad touch different banks: the upper
-        // two take the pair's second key first, and the interleave undoes it
-        const int kf = 2 * t + (t >> 1), ks = 2 * t + 1 - (t >> 1);
-        const uint32_t sel_lo = t < 2 ? 0x5410u : 0x1054u, sel_hi = t < 2 ? 0x7632u : 0x3276u;
-        constexpr uint32_t kOne16 = 0x64006400u, kOneB = 0x43004300u, kMidB = 0x43084308u;  // 1024 | 128 | 136
-        int st = 0;
-        uint32_t phase = 0;
-        bool dead = false;
-        int64_t u = u_begin;
-        while (u < u_end) {
-            const TileAt at = tile_at(u, pb, p.B, p.G);
-            const int i1 = (int)min((int64_t)at.nt, at.i + (u_end - u));
-            const int L = p.seqlens[at.b];
-            make_queries<D>(p, at.b, at.g, L - 1, tail);
-            const float qsc = lds_f32(stail + C::OFF_QSC + gid * 4);
-            const uint32_t qhi = lds32(stail + C::OFF_QSUM + gid * 16 + t * 4);
-            const uint32_t qlo = lds32(stail + C::OFF_QSUM + 128 + gid * 16 + t * 4);
-            float oacc[2 * C::NG][4], cacc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int m = 0; m < 2 * C::NG; ++m) oacc[m][0] = oacc[m][1] = oacc[m][2] = oacc[m][3] = 0.f;
-            float m_run = -INFINITY, l_run = 0.f;
+        ++sent;
+        if (++s_send == n_stages) s_send = 0;
+    };
+    for (int s = 0; s < n_stages; ++s) send();
 
-            for (int i = at.i; i < i1; ++i) {
-                if (!dead && !__all_sync(0xffffffffu, mbar_wait(bar_full + 8 * st, phase, abort_flag, p.status)))
+    const int gid = lane >> 2, t = lane & 3;
+    // V words are read so that the four lanes of a quad touch different banks: the upper
+    // two take the pair's second key first, and the interleave undoes it
+    const int kf = 2 * t + (t >> 1), ks = 2 * t + 1 - (t >> 1);
+    const uint32_t sel_lo = t < 2 ? 0x5410u : 0x1054u, sel_hi = t < 2 ? 0x7632u : 0x3276u;
+    const uint32_t one_f16 = opaque(0x64006400u), one_bf16 = opaque(0x43004300u);  // 1024, 128
+    constexpr uint32_t kMid = 0x43084308u;                                         // 136
+    int st = 0;
+    bool dead = false;
+    int64_t u = u_begin;
+    while (u < u_end) {
+        const TileAt at = tile_at(u, pb, p.B, p.G);
+        const int i1 = (int)min((int64_t)at.nt, at.i + (u_end - u));
+        const int L = p.seqlens[at.b];
+        make_queries<D>(p, at.b, at.g, L - 1, tail);
+        const float2 qsc = ld<float2>(tail + C::OFF_QSC + t * 8);
+        const uint32_t qhi = ld<uint32_t>(tail + C::OFF_QSUM + gid * 16 + t * 4);
+        const uint32_t qlo = ld<uint32_t>(tail + C::OFF_QSUM + 128 + gid * 16 + t * 4);
+        const uint8_t* qfp = tail + C::OFF_QF + lane * 16;
+        const uint8_t* cip = tail + C::OFF_CINIT + t * 16;
+        float oacc[2 * C::NG][4], cacc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < 2 * C::NG; ++m) oacc[m][0] = oacc[m][1] = oacc[m][2] = oacc[m][3] = 0.f;
+        // softmax state of heads 2t and 2t + 1: the reference is the same in every lane that
+        // holds the head, the sum is over this lane's keys
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+
+        for (int i = at.i; i < i1; ++i) {
+            const int key0 = i * BT + 16 * warp;
+            if (pending >> st & 1u) {
+                if (!dead && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, phases >> st & 1u, abort_flag, p.status)))
                     dead = true;  // keep walking: the block's barriers need every warp
-                const int key0 = i * BT + 16 * warp;
-                if (!dead && key0 < L) {
-                    const uint32_t kb = sbase + st * C::STAGE_BYTES + warp * C::BLOCK_BYTES;
-                    const uint32_t vb = kb + C::TILE_BYTES;
-                    if (key0 + 16 > L) {  // rows past the end may hold anything: no scale, no centre
-                        uint16_t* par = reinterpret_cast<uint16_t*>(smem + st * C::STAGE_BYTES + C::TILE_BYTES +
-                                                                    warp * C::BLOCK_BYTES + 8 * D);
-                        for (int j = lane; j < 2 * C::NG * 16; j += 32)
-                            if (key0 + (j & 15) >= L) par[j] = 0;
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                if (!dead) {
+                    pending &= ~(1u << st);
+                    phases ^= 1u << st;
+                }
+            }
+            if (!dead && key0 < L) {
+                uint8_t* kb = ring + st * C::STAGE_BYTES;
+                uint8_t* vb = kb + C::BLOCK_BYTES;
+                if (key0 + 16 > L) {  // rows past the end may hold anything: no scale, no centre
+                    uint16_t* par = reinterpret_cast<uint16_t*>(vb + 8 * D);
+                    for (int j = lane; j < 2 * C::NG * 16; j += 32)
+                        if (key0 + (j & 15) >= L) par[j] = 0;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                // ---- S^T = K Q^T: lane holds keys gid and gid + 8, heads 2t and 2t + 1
+                const uint8_t* kc = kb + gid * 32 + t * 8;
+                const uint8_t* kp = kb + 8 * D + gid * 2;
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                {
+                    uint32_t ca = 0, cb = 0;  // centres of groups 2t, 2t + 1
+                    if (2 * t < C::NG) {
+                        const uint8_t* c = kb + 9 * D + t * 64 + gid * 2;
+                        ca = ld<uint16_t>(c) | ((uint32_t)ld<uint16_t>(c + 32) << 16);
+                        cb = ld<uint16_t>(c + 16) | ((uint32_t)ld<uint16_t>(c + 48) << 16);
                     }
-                    // ---- S = Q K^T, eight keys at a time: lane holds head gid, keys 2t and 2t + 1
-                    float x[2][2];
+                    mma_bf16_16816(s, ca, cb, ca, cb, qhi, qlo);
+                }
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        float s[4] = {0.f, 0.f, 0.f, 0.f};
-                        uint32_t cp = 0;
-                        if (2 * t < C::NG) {
-                            const uint32_t ca = kb + 9 * D + 2 * t * 32 + (nt * 8 + gid) * 2;
-                            cp = lds16(ca) | (lds16(ca + 32) << 16);
-                        }
-                        mma_bf16_16816(s, qhi, 0u, qlo, 0u, cp, cp);
+                for (int sl = 0; sl < D / 64; ++sl) {
+                    const uint2 wa = ld<uint2>(kc + sl * 512), wb = ld<uint2>(kc + sl * 512 + 256);
 #pragma unroll
-                        for (int sl = 0; sl < D / 64; ++sl) {
-                            const uint2 w = lds64(kb + sl * 512 + (nt * 8 + gid) * 32 + t * 8);
-                            uint32_t c[2] = {__byte_perm(w.x, w.y, 0x5410), __byte_perm(w.x, w.y, 0x7632)};
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int grp = 2 * sl + hf;
+                        const uint4 qf = ld<uint4>(qfp + grp * 512);
+                        const float4 ci = ld<float4>(cip + grp * 64);
+                        const uint32_t sel = hf ? 0x7632 : 0x5410;
+                        const uint32_t c0 = __byte_perm(wa.x, wa.y, sel), c1 = __byte_perm(wb.x, wb.y, sel);
+                        const uint32_t d0 = c0 >> 8, d1 = c1 >> 8;
+                        float a[4];
+                        mma_f16_16816(a, and_or<0x000F000Fu>(c0, one_f16), and_or<0x000F000Fu>(c1, one_f16),
+                                      and_or<0x00F000F0u>(c0, one_f16), and_or<0x00F000F0u>(c1, one_f16), qf.x, qf.y,
+                                      ci.x, ci.y, ci.z, ci.w);
+                        mma_f16_16816(a, and_or<0x000F000Fu>(d0, one_f16), and_or<0x000F000Fu>(d1, one_f16),
+                                      and_or<0x00F000F0u>(d0, one_f16), and_or<0x00F000F0u>(d1, one_f16), qf.z, qf.w,
+                                      a[0], a[1], a[2], a[3]);
+                        const float s0 = __uint_as_float((uint32_t)ld<uint16_t>(kp + grp * 32) << 16);
+                        const float s1 = __uint_as_float((uint32_t)ld<uint16_t>(kp + grp * 32 + 16) << 16);
+                        s[0] = fmaf(s0, a[0], s[0]);
+                        s[1] = fmaf(s0, a[1], s[1]);
+                        s[2] = fmaf(s1, a[2], s[2]);
+                        s[3] = fmaf(s1, a[3], s[3]);
+                    }
+                }
+                const bool live0 = key0 + gid < L, live1 = key0 + gid + 8 < L;
+                s[0] = live0 ? s[0] * qsc.x : -INFINITY;
+                s[1] = live0 ? s[1] * qsc.y : -INFINITY;
+                s[2] = live1 ? s[2] * qsc.x : -INFINITY;
+                s[3] = live1 ? s[3] * qsc.y : -INFINITY;
+                // ---- online softmax; the reference moves only when some logit is 2^8 above it
+                float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+                if (__any_sync(0xffffffffu, t0 > m_run[0] + 8.f || t1 > m_run[1] + 8.f)) {
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                const int grp = 2 * sl + hf;
-                                const uint4 qf = lds_v4(stail + C::OFF_QF + grp * 512 + lane * 16);
-                                const float ci = lds_f32(stail + C::OFF_CINIT + grp * 32 + gid * 4);
-                                float a[4] = {ci, ci, 0.f, 0.f};
-                                mma_f16_top(a, qf.x, qf.y, (c[hf] & 0x000F000Fu) | kOne16, (c[hf] & 0x00F000F0u) | kOne16);
-                                c[hf] >>= 8;
-                                mma_f16_top(a, qf.z, qf.w, (c[hf] & 0x000F000Fu) | kOne16, (c[hf] & 0x00F000F0u) | kOne16);
-                                const uint32_t sc = lds32(kb + 8 * D + grp * 32 + nt * 16 + t * 4);
-                                s[0] = fmaf(bf16_lo(sc), a[0], s[0]);
-                                s[1] = fmaf(bf16_hi(sc), a[1], s[1]);
+                    for (int o = 4; o < 32; o <<= 1) {
+                        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, o));
+                        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+                    }
+                    t0 = fmaxf(t0, m_run[0]);
+                    t1 = fmaxf(t1, m_run[1]);
+                    const float a0 = t0 == m_run[0] ? 1.f : ex2_approx(m_run[0] - t0);
+                    const float a1 = t1 == m_run[1] ? 1.f : ex2_approx(m_run[1] - t1);
+                    m_run[0] = t0;
+                    m_run[1] = t1;
+                    l_run[0] *= a0;
+                    l_run[1] *= a1;
+#pragma unroll
+                    for (int m = 0; m < 2 * C::NG; ++m) {
+                        oacc[m][0] *= a0;
+                        oacc[m][1] *= a1;
+                        oacc[m][2] *= a0;
+                        oacc[m][3] *= a1;
+                    }
+                    cacc[0] *= a0;
+                    cacc[1] *= a1;
+                }
+                uint32_t pr[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t w = pack_bf16x2(ex2_approx(s[2 * k] - m_run[0]), ex2_approx(s[2 * k + 1] - m_run[1]));
+                    l_run[0] += bf16_lo(w);  // the sum of the weights as they are used
+                    l_run[1] += bf16_hi(w);
+                    pr[k] = transpose8x8(w);  // head gid, keys 8k + 2t, 8k + 2t + 1
+                }
+                // ---- centres: row g of A is group g
+                {
+                    const uint8_t* ca = vb + 9 * D + gid * 32 + t * 4;
+                    uint32_t a0 = 0, a2 = 0;
+                    if (gid < C::NG) {
+                        a0 = ld<uint32_t>(ca);
+                        a2 = ld<uint32_t>(ca + 16);
+                    }
+                    mma_bf16_16816(cacc, a0, 0u, a2, 0u, pr[0], pr[1]);
+                }
+                // ---- O^T += V^T P^T
+                const uint8_t* vf = vb + gid * 4 + kf * 32;
+                const uint8_t* vs = vb + gid * 4 + ks * 32;
+                const uint8_t* vp = vb + 8 * D + t * 4;
+#pragma unroll
+                for (int sl = 0; sl < D / 64; ++sl) {
+                    const uint32_t f0 = ld<uint32_t>(vf + sl * 512), s0 = ld<uint32_t>(vs + sl * 512);
+                    const uint32_t f1 = ld<uint32_t>(vf + sl * 512 + 256), s1 = ld<uint32_t>(vs + sl * 512 + 256);
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int grp = 2 * sl + hf;
+                        const uint32_t sel = hf ? sel_hi : sel_lo;
+                        const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
+                        const uint32_t p0 = mul_bf16x2(pr[0], ld<uint32_t>(vp + grp * 32));
+                        const uint32_t p1 = mul_bf16x2(pr[1], ld<uint32_t>(vp + grp * 32 + 16));
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            uint32_t a[4];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int sh = 4 * (2 * m + k);
+                                a[k] = sub_bf16x2(and_or<0x000F000Fu>(w0 >> sh, one_bf16), kMid);
+                                a[2 + k] = sub_bf16x2(and_or<0x000F000Fu>(w1 >> sh, one_bf16), kMid);
                             }
-                        }
-                        const int key = key0 + nt * 8 + 2 * t;
-                        x[nt][0] = key < L ? s[0] * qsc : -INFINITY;
-                        x[nt][1] = key + 1 < L ? s[1] * qsc : -INFINITY;
-                    }
-                    // ---- online softmax; the reference moves only when a head's maximum grew by 2^8
-                    float tmax = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-                    tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-                    tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-                    if (__any_sync(0xffffffffu, tmax > m_run + 8.f)) {
-                        const float m_new = fmaxf(m_run, tmax);
-                        const float alpha = m_run == m_new ? 1.f : ex2_approx(m_run - m_new);
-                        m_run = m_new;
-                        l_run *= alpha;
-                        const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * t);
-                        const float a_hi = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-#pragma unroll
-                        for (int m = 0; m < 2 * C::NG; ++m) {
-                            oacc[m][0] *= a_lo;
-                            oacc[m][1] *= a_hi;
-                            oacc[m][2] *= a_lo;
-                            oacc[m][3] *= a_hi;
-                        }
-                        cacc[0] *= a_lo;
-                        cacc[1] *= a_hi;
-                    }
-                    uint32_t pr[2];
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        pr[nt] = pack_bf16x2(ex2_approx(x[nt][0] - m_run), ex2_approx(x[nt][1] - m_run));
-                        l_run += bf16_lo(pr[nt]) + bf16_hi(pr[nt]);  // the sum of the weights as they are used
-                    }
-                    // ---- centres: row g of A is group g
-                    {
-                        const uint32_t ca = vb + 9 * D + gid * 32 + t * 4;
-                        const bool real = gid < C::NG;
-                        mma_bf16_16816(cacc, real ? lds32(ca) : 0u, 0u, real ? lds32(ca + 16) : 0u, 0u, pr[0], pr[1]);
-                    }
-                    // ---- O^T += V^T P^T
-#pragma unroll
-                    for (int sl = 0; sl < D / 64; ++sl) {
-                        const uint32_t va = vb + sl * 512 + gid * 4;
-                        const uint32_t f0 = lds32(va + kf * 32), s0 = lds32(va + ks * 32);
-                        const uint32_t f1 = lds32(va + 256 + kf * 32), s1 = lds32(va + 256 + ks * 32);
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int grp = 2 * sl + hf;
-                            const uint32_t sel = hf ? sel_hi : sel_lo;
-                            const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
-                            const uint32_t sa = vb + 8 * D + grp * 32 + t * 4;
-                            const uint32_t p0 = mul_bf16x2(pr[0], lds32(sa)), p1 = mul_bf16x2(pr[1], lds32(sa + 16));
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                uint32_t a[4];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int sh = 4 * (2 * m + k);
-                                    a[k] = sub_bf16x2(((w0 >> sh) & 0x000F000Fu) | kOneB, kMidB);
-                                    a[2 + k] = sub_bf16x2(((w1 >> sh) & 0x000F000Fu) | kOneB, kMidB);
-                                }
-                                mma_bf16_16816(oacc[2 * grp + m], a[0], a[1], a[2], a[3], p0, p1);
-                            }
+                            mma_bf16_16816(oacc[2 * grp + m], a[0], a[1], a[2], a[3], p0, p1);
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_empty + 8 * st);
-                if (++st == n_stages) {
-                    st = 0;
-                    phase ^= 1u;
-                }
             }
-
-            // -------- end of the piece: merge the four warps, then finish or hand over
-            l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-            l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-            float* ml = reinterpret_cast<float*>(tail + C::OFF_ML);
-            float* obuf = reinterpret_cast<float*>(tail + C::OFF_OBUF);
-            if (t == 0) {
-                ml[(warp * 8 + gid) * 2] = m_run;
-                ml[(warp * 8 + gid) * 2 + 1] = l_run;
-            }
-            named_barrier(1, 32 * NCW);
-            // weight of this warp's state for the lane's two heads
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = -INFINITY;
-                for (int w = 0; w < NCW; ++w) mx = fmaxf(mx, ml[(w * 8 + 2 * t + e) * 2]);
-                const float mine = ml[(warp * 8 + 2 * t + e) * 2];
-                f[e] = mine == -INFINITY ? 0.f : ex2_approx(mine - mx);
-            }
-            for (int w = 0; w < NCW; ++w) {
-                if (w == warp) {
-#pragma unroll
-                    for (int grp = 0; grp < C::NG; ++grp) {
-                        const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * grp + t);
-                        const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * grp + t);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int h = 2 * t + e;
-                            const float c = e ? c1 : c0;
-                            float4* at4 = reinterpret_cast<float4*>(obuf + h * C::OROW + grp * 32 + gid * 4);
-                            if (h < r) {
-                                float4 o = w ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (f[e] != 0.f) {
-                                    o.x = fmaf(f[e], oacc[2 * grp][e] + c, o.x);
-                                    o.y = fmaf(f[e], oacc[2 * grp][2 + e] + c, o.y);
-                                    o.z = fmaf(f[e], oacc[2 * grp + 1][e] + c, o.z);
-                                    o.w = fmaf(f[e], oacc[2 * grp + 1][2 + e] + c, o.w);
-                                }
-                                *at4 = o;
-                            }
-                        }
-                    }
-                }
-                named_barrier(1, 32 * NCW);
-            }
-            const bool alone = at.i == 0 && i1 == at.nt;
-            const int64_t seg = (int64_t)at.b * p.G + at.g;
-            float* ps = p.part + ((int64_t)blockIdx.x + seg) * (int64_t)(2 * r + r * D);
-            for (int h = 0; h < r; ++h) {
-                float mx = -INFINITY, l = 0.f;
-                for (int w = 0; w < NCW; ++w) mx = fmaxf(mx, ml[(w * 8 + h) * 2]);
-                for (int w = 0; w < NCW; ++w) {
-                    const float mw = ml[(w * 8 + h) * 2];
-                    l += mw == -INFINITY ? 0.f : ex2_approx(mw - mx) * ml[(w * 8 + h) * 2 + 1];
-                }
-                for (int e = threadIdx.x; e < D; e += 32 * NCW) {
-                    const float o = obuf[h * C::OROW + e];
-                    if (alone) {
-                        static_cast<bf16*>(p.out)[((int64_t)at.b * p.H + at.g * r + h) * D + e] =
-                            __float2bfloat16_rn(gated(p, at.b, at.g * r + h, e, o / l));
-                    } else {
-                        ps[2 * r + h * D + e] = o;
-                    }
-                }
-                if (!alone && threadIdx.x == 0) {
-                    ps[h] = mx;
-                    ps[r + h] = l;
-                }
-            }
-            u += i1 - at.i;
+            __syncwarp();
+            if (!dead) send();  // into the stage just read
+            if (++st == n_stages) st = 0;
         }
+
+        // -------- end of the piece: merge the four warps, then finish or hand over
+        float* ml = reinterpret_cast<float*>(tail + C::OFF_ML);
+        float* obuf = reinterpret_cast<float*>(tail + C::OFF_OBUF);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], o);
+            l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], o);
+        }
+        if (gid == 0) reinterpret_cast<float4*>(ml)[warp * 4 + t] = make_float4(m_run[0], l_run[0], m_run[1], l_run[1]);
+        __syncthreads();
+        // weight of this warp's state for the lane's two heads
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + 2 * t + e) * 2]);
+            const float mine = ml[(warp * 8 + 2 * t + e) * 2];
+            f[e] = mine == -INFINITY ? 0.f : ex2_approx(mine - mx);
+        }
+        for (int w = 0; w < NW; ++w) {
+            if (w == warp) {
+#pragma unroll
+                for (int grp = 0; grp < C::NG; ++grp) {
+                    const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * grp + t);
+                    const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * grp + t);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int h = 2 * t + e;
+                        const float c = e ? c1 : c0;
+                        float4* at4 = reinterpret_cast<float4*>(obuf + h * C::OROW + grp * 32 + gid * 4);
+                        if (h < r) {
+                            float4 o = w ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (f[e] != 0.f) {
+                                o.x = fmaf(f[e], oacc[2 * grp][e] + c, o.x);
+                                o.y = fmaf(f[e], oacc[2 * grp][2 + e] + c, o.y);
+                                o.z = fmaf(f[e], oacc[2 * grp + 1][e] + c, o.z);
+                                o.w = fmaf(f[e], oacc[2 * grp + 1][2 + e] + c, o.w);
+                            }
+                            *at4 = o;
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        const bool alone = at.i == 0 && i1 == at.nt;
+        const int64_t seg = (int64_t)at.b * p.G + at.g;
+        float* ps = p.part + ((int64_t)blockIdx.x + seg) * (int64_t)(2 * r + r * D);
+        for (int h = 0; h < r; ++h) {
+            float mx = -INFINITY, l = 0.f;
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + h) * 2]);
+            for (int w = 0; w < NW; ++w) {
+                const float mw = ml[(w * 8 + h) * 2];
+                l += mw == -INFINITY ? 0.f : ex2_approx(mw - mx) * ml[(w * 8 + h) * 2 + 1];
+            }
+            for (int e = threadIdx.x; e < D; e += THREADS) {
+                const float o = obuf[h * C::OROW + e];
+                if (alone) {
+                    static_cast<bf16*>(p.out)[((int64_t)at.b * p.H + at.g * r + h) * D + e] =
+                        __float2bfloat16_rn(gated(p, at.b, at.g * r + h, e, o / l));
+                } else {
+                    ps[2 * r + h * D + e] = o;
+                }
+            }
+            if (!alone && threadIdx.x == 0) {
+                ps[h] = mx;
+                ps[r + h] = l;
+            }
+        }
+        u += i1 - at.i;
     }
-    __syncthreads();
+    // every copy that was sent lands before the block leaves (none is left unless a wait ran out)
+    for (int s = 0; s < n_stages; ++s)
+        if (pending >> s & 1u) mbar_wait_drain(bars + 8 * s, phases >> s & 1u, p.status);
 }
 
 // Merge the partial states of one (sequence, KV head) that several CTAs share and apply
@@ -669,9 +691,9 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
                      cudaEvent_t ev_stop) {
     using C = QdCfg<D>;
     const int n_ctas = C::CTAS_PER_SM * p.n_sms;
-    // ring depth: what an SM's 228 KB (1 KB of it reserved per CTA) leave for each CTA
+    // ring depth: what an SM's 228 KB (1 KB of it reserved per CTA) leave for each warp
     const int tail = tail_bytes<D>(p.B, p.H / p.G, p.rd);
-    int stages = ((228 * 1024) / C::CTAS_PER_SM - 1024 - tail) / C::STAGE_BYTES;
+    int stages = ((228 * 1024) / C::CTAS_PER_SM - 1024 - tail) / (NW * C::STAGE_BYTES);
     stages = stages < 2 ? 2 : stages > C::MAX_STAGES ? C::MAX_STAGES : stages;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(qdecode_split_kernel<D>), 227 * 1024);
     if (e != cudaSuccess) return e;
@@ -683,7 +705,7 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
     cfg.stream = stream;
     cfg.gridDim = dim3((unsigned)n_ctas);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = (size_t)(stages * C::STAGE_BYTES + tail);
+    cfg.dynamicSmemBytes = (size_t)(NW * stages * C::STAGE_BYTES + tail);
     cfg.numAttrs = after_write ? 1 : 0;
     if (ev_start) cudaEventRecord(ev_start, stream);
     e = cudaLaunchKernelEx(&cfg, qdecode_split_kernel<D>, p, stages, after_write);
