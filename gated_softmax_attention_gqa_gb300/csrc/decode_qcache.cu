@@ -41,6 +41,9 @@ namespace {
 constexpr int BT = 64;  // keys per tile
 constexpr int NW = 4;   // warps, one per 16-token block of a tile
 constexpr int THREADS = 32 * NW;
+// What starting and merging a (sequence, KV head) piece costs, in tiles: the work split
+// counts it, so a CTA with many short sequences gets fewer tiles.
+constexpr int kPieceTiles = 2;
 
 template <int D>
 struct QdCfg {
@@ -56,7 +59,8 @@ struct QdCfg {
     static constexpr int OFF_QSUM = OFF_CINIT + NG * 64;     // bf16 [2][8 heads][8 groups], high and low parts
     static constexpr int OFF_QSC = OFF_QSUM + 256;           // float [8] logit scale of a head
     static constexpr int OFF_ML = OFF_QSC + 32;              // float [NW][8][2] the warps' (max, sum)
-    static constexpr int OFF_BAR = OFF_ML + NW * 64;         // mbarrier [NW][MAX_STAGES]
+    static constexpr int OFF_TOT = OFF_ML + NW * 64;         // float [8][2] the merged (max, sum)
+    static constexpr int OFF_BAR = OFF_TOT + 64;             // mbarrier [NW][MAX_STAGES]
     static constexpr int OFF_MISC = OFF_BAR + NW * 8 * MAX_STAGES;
     static constexpr int OFF_RED = OFF_MISC + 16;            // int [NW] scan scratch
     static constexpr int OFF_OBUF = OFF_RED + 16;            // float [r][OROW]; the sine table (rd/2 float2) before it
@@ -70,18 +74,27 @@ __host__ __device__ int obuf_bytes(int r, int rd) {
 }
 template <int D>
 __host__ __device__ int tail_bytes(int B, int r, int rd) {
-    return QdCfg<D>::OFF_OBUF + obuf_bytes<D>(r, rd) + 4 * (B + 1);
+    return QdCfg<D>::OFF_OBUF + obuf_bytes<D>(r, rd) + 4 * (2 * B + 1);
 }
 
 __device__ __forceinline__ int seq_tiles(int L, int Lmax) { return (L >= 1 && L <= Lmax) ? (L + BT - 1) / BT : 0; }
 
-// Exclusive prefix of per-sequence tile counts into pb[0..B]; all threads.
-__device__ void tile_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, int* red) {
+// Work units of one KV head of a sequence: its tiles and, ahead of them, kPieceTiles that
+// stand for the piece itself.
+__device__ __forceinline__ int seq_units(int L, int Lmax) {
+    const int n = seq_tiles(L, Lmax);
+    return n ? n + kPieceTiles : 0;
+}
+
+// Exclusive prefix of the sequences' units into pb[0..B], and their lengths; all threads.
+__device__ void unit_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, int* lens, int* red) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int carry = 0;
     for (int base = 0; base < B; base += THREADS) {
         const int i = base + tid;
-        int v = i < B ? seq_tiles(seqlens[i], Lmax) : 0;
+        const int L = i < B ? seqlens[i] : 0;
+        int v = seq_units(L, Lmax);
+        if (i < B) lens[i] = L;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int n = __shfl_up_sync(0xffffffffu, v, o);
@@ -102,7 +115,11 @@ __device__ void tile_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, in
     __syncthreads();
 }
 
-// Tile u of the global list: sequence b, group g, tile i of its nt.
+// CTAs that share U units: no more than there are, so none between two that hold parts of
+// a sequence is empty.
+__device__ __forceinline__ int active_ctas(int64_t U, int n_ctas) { return U < n_ctas ? (int)U : n_ctas; }
+
+// Unit u of the global list: sequence b, KV head g, tile i of nt (negative: the piece's own units).
 struct TileAt {
     int b, g, i, nt;
 };
@@ -114,10 +131,11 @@ __device__ __forceinline__ TileAt tile_at(int64_t u, const int* pb, int B, int G
     }
     TileAt t;
     t.b = lo;
-    t.nt = pb[lo + 1] - pb[lo];
-    const int rel = (int)(u - (int64_t)G * pb[lo]);
-    t.g = rel / t.nt;
-    t.i = rel % t.nt;
+    const int nu = pb[lo + 1] - pb[lo];
+    const int64_t rel = u - (int64_t)G * pb[lo];
+    t.g = rel < INT32_MAX ? (int)rel / nu : (int)(rel / nu);
+    t.i = (int)(rel - (int64_t)t.g * nu) - kPieceTiles;
+    t.nt = nu - kPieceTiles;
     return t;
 }
 
@@ -189,6 +207,13 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
     constexpr int LPH = D / 8, HPW = 32 / LPH;  // lanes per head, heads per warp and pass
     const int r = p.H / p.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float2* table = reinterpret_cast<float2*>(tail + C::OFF_OBUF);
+    const int u = lane % LPH, e0 = 8 * u, hw = warp * HPW + lane / LPH;
+    auto load_q = [&](int h) {
+        return *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.q) + b * p.q_seq_stride +
+                                               (int64_t)(g * r + (h < r ? h : 0)) * p.q_head_stride + e0);
+    };
+    const uint4 wraw = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.qnorm_w) + e0);
+    uint4 qraw = load_q(hw);
     __syncthreads();  // the previous piece has left the fragments and the merge buffer
     for (int i = tid; i < (p.rd >> 1); i += THREADS) {
         float s, c;
@@ -196,14 +221,14 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
         table[i] = make_float2(s, c);
     }
     __syncthreads();
-    const int half = p.rd >> 1, u = lane % LPH, e0 = 8 * u;
+    const int half = p.rd >> 1;
     for (int h0 = warp * HPW; h0 < r; h0 += NW * HPW) {
         const int h = h0 + lane / LPH;
         const bool live = h < r;
         float x[8], w[8], ss = 0.f;
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.q) + b * p.q_seq_stride +
-                                                (int64_t)(g * r + (live ? h : 0)) * p.q_head_stride + e0), x);
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.qnorm_w) + e0), w);
+        unpack8(qraw, x);
+        unpack8(wraw, w);
+        if (h0 + NW * HPW < r) qraw = load_q(h + NW * HPW);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             ss = fmaf(x[i], x[i], ss);
@@ -270,6 +295,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = p.H / p.G, Lmax = p.max_pages * p.page_size;
     int* pb = reinterpret_cast<int*>(tail + C::OFF_OBUF + obuf_bytes<D>(r, p.rd));
+    int* lens = pb + p.B + 1;
     uint8_t* ring = smem + warp * n_stages * C::STAGE_BYTES;
     const uint32_t bars = smem_u32(tail + C::OFF_BAR) + warp * 8 * C::MAX_STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
@@ -282,11 +308,13 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     if (threadIdx.x == 0) *abort_flag = 0;
     // rows of heads that do not exist stay zero
     for (int i = threadIdx.x; i < C::OFF_ML / 4; i += THREADS) reinterpret_cast<uint32_t*>(tail)[i] = 0u;
-    tile_prefix(p.seqlens, p.B, Lmax, pb, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
+    unit_prefix(p.seqlens, p.B, Lmax, pb, lens, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
 
-    const int64_t T = (int64_t)p.G * pb[p.B];
-    const int64_t u_begin = (int64_t)blockIdx.x * T / gridDim.x;
-    const int64_t u_end = (int64_t)(blockIdx.x + 1) * T / gridDim.x;
+    const int64_t U = (int64_t)p.G * pb[p.B];
+    const int N = active_ctas(U, gridDim.x);
+    if (blockIdx.x >= N) return;
+    const int64_t u_begin = blockIdx.x * U / N;
+    const int n_units = (int)((blockIdx.x + 1) * U / N - u_begin);
     const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * C::BLOCK_BYTES;
     const int bpp = p.page_size / kQcBlock;
     if (after_write) {  // the appended rows were written by the kernel before this one
@@ -294,21 +322,21 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         fence_proxy_async_global();
     }
 
-    // ---- the warp's copies run n_stages tiles ahead.  Lane j holds the address of the
-    // warp's block of tile batch + j (0: past the sequence's end), 32 table entries a time.
-    int64_t batch = u_begin, sent = u_begin;
+    // ---- the warp's copies run n_stages units ahead.  Lane j holds the address of the
+    // warp's block of unit batch + j (0: no tile, or past the sequence's end), 32 table
+    // entries a time.
+    int batch = 0, sent = 0, s_send = 0;
     uint64_t src = 0;
     uint32_t pending = 0, phases = 0;  // per stage: a copy is under way; parity of its barrier
-    int s_send = 0;
-    auto send = [&]() {  // all lanes; tile `sent` into stage s_send
-        if (sent >= u_end) return;
-        if (sent == u_begin || sent == batch + 32) {
+    auto send = [&]() {  // all lanes; unit `sent` into stage s_send
+        if (sent >= n_units) return;
+        if ((sent & 31) == 0) {
             batch = sent;
             src = 0;
-            if (batch + lane < u_end) {
-                const TileAt t = tile_at(batch + lane, pb, p.B, p.G);
+            if (batch + lane < n_units) {
+                const TileAt t = tile_at(u_begin + batch + lane, pb, p.B, p.G);
                 const int blk = t.i * (BT / kQcBlock) + warp;
-                if (blk * kQcBlock < p.seqlens[t.b]) {
+                if (t.i >= 0 && blk * kQcBlock < lens[t.b]) {
                     int page = p.block_table[(int64_t)t.b * p.max_pages + blk / bpp];
                     if (page < 0 || page >= p.num_pages) {
                         atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
@@ -318,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                 }
             }
         }
-        const uint64_t a = __shfl_sync(0xffffffffu, src, (int)(sent - batch));
+        const uint64_t a = __shfl_sync(0xffffffffu, src, sent - batch);
         if (a) {
             if (lane == 0) {
                 const uint32_t bar = bars + 8 * s_send, dst = smem_u32(ring + s_send * C::STAGE_BYTES);
@@ -342,11 +370,18 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     constexpr uint32_t kMid = 0x43084308u;                                         // 136
     int st = 0;
     bool dead = false;
-    int64_t u = u_begin;
-    while (u < u_end) {
-        const TileAt at = tile_at(u, pb, p.B, p.G);
-        const int i1 = (int)min((int64_t)at.nt, at.i + (u_end - u));
-        const int L = p.seqlens[at.b];
+    TileAt at = tile_at(u_begin, pb, p.B, p.G);
+    for (int n = 0; n < n_units;) {
+        const int i1 = min(at.nt, at.i + (n_units - n));  // this CTA's tiles of the piece: [i0, i1)
+        const int i0 = max(at.i, 0);
+        const int L = lens[at.b];
+        n += i1 - at.i;
+        for (int i = at.i; i < min(i0, i1); ++i) {  // the piece's own units hold no tile
+            send();
+            if (++st == n_stages) st = 0;
+        }
+        if (i1 <= 0) break;
+        const bool alone = i0 == 0 && i1 == at.nt;
         make_queries<D>(p, at.b, at.g, L - 1, tail);
         const float2 qsc = ld<float2>(tail + C::OFF_QSC + t * 8);
         const uint32_t qhi = ld<uint32_t>(tail + C::OFF_QSUM + gid * 16 + t * 4);
@@ -360,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         // holds the head, the sum is over this lane's keys
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
-        for (int i = at.i; i < i1; ++i) {
+        for (int i = i0; i < i1; ++i) {
             const int key0 = i * BT + 16 * warp;
             if (pending >> st & 1u) {
                 if (!dead && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, phases >> st & 1u, abort_flag, p.status)))
@@ -517,61 +552,72 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float mx = -INFINITY;
+#pragma unroll
             for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + 2 * t + e) * 2]);
             const float mine = ml[(warp * 8 + 2 * t + e) * 2];
             f[e] = mine == -INFINITY ? 0.f : ex2_approx(mine - mx);
         }
-        for (int w = 0; w < NW; ++w) {
-            if (w == warp) {
+        if (threadIdx.x < 8) {  // the merged maximum and sum of head threadIdx.x
+            float mx = -INFINITY, l = 0.f;
 #pragma unroll
-                for (int grp = 0; grp < C::NG; ++grp) {
-                    const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * grp + t);
-                    const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * grp + t);
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + threadIdx.x) * 2]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int h = 2 * t + e;
-                        const float c = e ? c1 : c0;
-                        float4* at4 = reinterpret_cast<float4*>(obuf + h * C::OROW + grp * 32 + gid * 4);
-                        if (h < r) {
-                            float4 o = w ? *at4 : make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (f[e] != 0.f) {
-                                o.x = fmaf(f[e], oacc[2 * grp][e] + c, o.x);
-                                o.y = fmaf(f[e], oacc[2 * grp][2 + e] + c, o.y);
-                                o.z = fmaf(f[e], oacc[2 * grp + 1][e] + c, o.z);
-                                o.w = fmaf(f[e], oacc[2 * grp + 1][2 + e] + c, o.w);
-                            }
-                            *at4 = o;
+            for (int w = 0; w < NW; ++w) {
+                const float mw = ml[(w * 8 + threadIdx.x) * 2];
+                l += mw == -INFINITY ? 0.f : ex2_approx(mw - mx) * ml[(w * 8 + threadIdx.x) * 2 + 1];
+            }
+            reinterpret_cast<float2*>(tail + C::OFF_TOT)[threadIdx.x] = make_float2(mx, l);
+        }
+        // four rounds; in each the warps add to different quarters of the features
+        constexpr int MQ = C::NG / 2;  // row tiles a quarter
+#pragma unroll 1
+        for (int k = 0; k < NW; ++k) {
+            const int quarter = (warp + k) & 3;
+#pragma unroll
+            for (int m = 0; m < 2 * C::NG; ++m) {
+                if (m / MQ != quarter) continue;
+                const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * (m >> 1) + t);
+                const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * (m >> 1) + t);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = 2 * t + e;
+                    float2* at2 = reinterpret_cast<float2*>(obuf + h * C::OROW + (m >> 1) * 32 + gid * 4 + (m & 1) * 2);
+                    if (h < r) {
+                        float2 o = k ? *at2 : make_float2(0.f, 0.f);
+                        if (f[e] != 0.f) {
+                            o.x = fmaf(f[e], oacc[m][e] + (e ? c1 : c0), o.x);
+                            o.y = fmaf(f[e], oacc[m][2 + e] + (e ? c1 : c0), o.y);
                         }
+                        *at2 = o;
                     }
                 }
             }
             __syncthreads();
         }
-        const bool alone = at.i == 0 && i1 == at.nt;
-        const int64_t seg = (int64_t)at.b * p.G + at.g;
-        float* ps = p.part + ((int64_t)blockIdx.x + seg) * (int64_t)(2 * r + r * D);
-        for (int h = 0; h < r; ++h) {
-            float mx = -INFINITY, l = 0.f;
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + h) * 2]);
-            for (int w = 0; w < NW; ++w) {
-                const float mw = ml[(w * 8 + h) * 2];
-                l += mw == -INFINITY ? 0.f : ex2_approx(mw - mx) * ml[(w * 8 + h) * 2 + 1];
+        const float2* tot = reinterpret_cast<const float2*>(tail + C::OFF_TOT);
+        const int h0 = at.g * r;
+        if (alone) {
+            for (int j = threadIdx.x; j < r * D; j += THREADS) {
+                const int h = j / D, e = j % D;
+                static_cast<bf16*>(p.out)[((int64_t)at.b * p.H + h0) * D + j] =
+                    __float2bfloat16_rn(gated(p, at.b, h0 + h, e, obuf[h * C::OROW + e] / tot[h].y));
             }
-            for (int e = threadIdx.x; e < D; e += THREADS) {
-                const float o = obuf[h * C::OROW + e];
-                if (alone) {
-                    static_cast<bf16*>(p.out)[((int64_t)at.b * p.H + at.g * r + h) * D + e] =
-                        __float2bfloat16_rn(gated(p, at.b, at.g * r + h, e, o / l));
-                } else {
-                    ps[2 * r + h * D + e] = o;
-                }
-            }
-            if (!alone && threadIdx.x == 0) {
-                ps[h] = mx;
-                ps[r + h] = l;
+        } else {
+            float* ps = p.part + ((int64_t)blockIdx.x + (int64_t)at.b * p.G + at.g) * (int64_t)(2 * r + r * D);
+            for (int j = threadIdx.x; j < r * D; j += THREADS) ps[2 * r + j] = obuf[(j / D) * C::OROW + j % D];
+            if (threadIdx.x < r) {
+                ps[threadIdx.x] = tot[threadIdx.x].x;
+                ps[r + threadIdx.x] = tot[threadIdx.x].y;
             }
         }
-        u += i1 - at.i;
+        // the next piece: the next KV head, or the next sequence that holds anything
+        at.i = -kPieceTiles;
+        if (++at.g == p.G) {
+            at.g = 0;
+            do { ++at.b; } while (at.b < p.B && pb[at.b + 1] == pb[at.b]);
+            if (at.b == p.B) break;
+            at.nt = pb[at.b + 1] - pb[at.b] - kPieceTiles;
+        }
     }
     // every copy that was sent lands before the block leaves (none is left unless a wait ran out)
     for (int s = 0; s < n_stages; ++s)
@@ -602,9 +648,9 @@ __global__ void __launch_bounds__(256) qdecode_combine_kernel(const __grid_const
         if (threadIdx.x == 0 && g == 0) atomicOr(p.status, GATTN_DEVICE_BAD_SEQLEN);
         return;
     }
-    int before = 0, total = 0;  // tiles ahead of this sequence, and of all
+    int before = 0, total = 0;  // units ahead of this sequence, and of all
     for (int i = lane; i < p.B; i += 32) {
-        const int n = seq_tiles(p.seqlens[i], Lmax);
+        const int n = seq_units(p.seqlens[i], Lmax);
         total += n;
         if (i < b) before += n;
     }
@@ -613,10 +659,11 @@ __global__ void __launch_bounds__(256) qdecode_combine_kernel(const __grid_const
         before += __shfl_xor_sync(0xffffffffu, before, o);
         total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    const int64_t T = (int64_t)p.G * total, N = n_ctas;
-    const int64_t u0 = (int64_t)p.G * before + (int64_t)g * nt, u1 = u0 + nt - 1;
-    // CTA c holds tiles [c T / N, (c + 1) T / N): the one that holds tile x
-    const int64_t c0 = ((u0 + 1) * N - 1) / T, c1 = ((u1 + 1) * N - 1) / T;
+    const int64_t U = (int64_t)p.G * total;
+    const int N = active_ctas(U, n_ctas);
+    const int64_t u0 = (int64_t)p.G * before + (int64_t)g * (nt + kPieceTiles) + kPieceTiles, u1 = u0 + nt - 1;
+    // CTA c holds units [c U / N, (c + 1) U / N): the ones that hold the first and the last tile
+    const int64_t c0 = ((u0 + 1) * N - 1) / U, c1 = ((u1 + 1) * N - 1) / U;
     const int n_parts = 8 / r, h = warp % r, part = warp / r, stride = 2 * r + r * D;
     const float* part0 = p.part + (c0 + (int64_t)b * p.G + g) * (int64_t)stride;
     const int n_slots = (int)(c1 - c0) + 1;
@@ -632,8 +679,7 @@ __global__ void __launch_bounds__(256) qdecode_combine_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
                 const int s = s0 + j * n_parts;
-                // fewer tiles than CTAs: a CTA between two that hold tiles may hold none
-                const bool live = s < n_slots && (c0 + s) * T / N < (c0 + s + 1) * T / N;
+                const bool live = s < n_slots;
                 const float* ps = part0 + (int64_t)(live ? s : 0) * stride;
                 ms[j] = live ? ps[h] : -INFINITY;
                 ls[j] = live ? ps[r + h] : 0.f;

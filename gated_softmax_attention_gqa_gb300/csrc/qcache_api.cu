@@ -169,6 +169,8 @@ gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const voi
     if (st != GATTN_OK) return st;
     if ((st = check_rope(d, rotary_dim, rope_base, eps)) != GATTN_OK) return st;
     if (H / G > 8 || B > decode_max_batch()) return GATTN_ERR_UNSUPPORTED;
+    // the kernels count the batch's 64-key tiles (and a few per head and sequence) in 31 bits
+    if ((int64_t)B * G * ((int64_t)max_pages * page_size / 64 + 8) > INT32_MAX) return GATTN_ERR_UNSUPPORTED;
     if (!aligned(seqlens, 4) || !aligned(out, 16)) return GATTN_ERR_INVALID_ARG;
     const bool append = k_new || v_new;
     if (append && (!k_new || !v_new || !knorm_w)) return GATTN_ERR_INVALID_ARG;
