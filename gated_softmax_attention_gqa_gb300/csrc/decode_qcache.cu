@@ -7,10 +7,10 @@
 // of the bandwidth is reached.
 //
 //   qdecode_split_kernel  persistent, a few CTAs of four warps per SM.  The (sequence, KV
-//       head) pairs are cut into 64-key tiles and the global tile list into equal
-//       contiguous ranges, one per CTA.  Warp w owns 16-token block w of every tile: it
-//       copies the block's K and V bytes into a ring of its own with two bulk copies, a
-//       few tiles ahead, and keeps its own softmax state, so the warps meet only at the
+//       head) pairs are cut into tiles of 64 (d = 256) or 128 keys and the global tile list
+//       into equal contiguous ranges, one per CTA.  Each warp owns one or two 16-token
+//       blocks of every tile: it copies their K and V bytes into a ring of its own with
+//       bulk copies, a few tiles ahead, and keeps its own softmax state, so the warps meet only at the
 //       end of a piece, where they are merged in shared memory.  (A producer warp for the
 //       four cost a fifth warp's registers, which the accumulators need: 128 a thread
 //       spilled, and 64 sequences of 16k-32k tokens took 432 us.)
@@ -38,8 +38,7 @@
 namespace gattn {
 namespace {
 
-constexpr int BT = 64;  // keys per tile
-constexpr int NW = 4;   // warps, one per 16-token block of a tile
+constexpr int NW = 4;  // warps, each with its own 16-token blocks of every tile
 constexpr int THREADS = 32 * NW;
 // What starting and merging a (sequence, KV head) piece costs, in tiles: the work split
 // counts it, so a CTA with many short sequences gets fewer tiles.
@@ -48,8 +47,13 @@ constexpr int kPieceTiles = 2;
 template <int D>
 struct QdCfg {
     static constexpr int NG = D / kQcGroup;             // scale groups
+    // 16-token blocks a warp takes of a tile.  Two share the copies, waits and softmax
+    // bookkeeping (some 250 instructions a step next to 230 a block at d = 128) and give the
+    // scheduler independent work; at d = 256 a deeper ring is worth more than that.
+    static constexpr int NB = D == 256 ? 1 : 2;
+    static constexpr int BT = NW * NB * kQcBlock;       // keys per tile
     static constexpr int BLOCK_BYTES = 10 * D;          // one 16-token block
-    static constexpr int STAGE_BYTES = 2 * BLOCK_BYTES; // a warp's K and V block
+    static constexpr int STAGE_BYTES = 2 * NB * BLOCK_BYTES;  // a warp's K and V blocks
     static constexpr int CTAS_PER_SM = D == 256 ? 3 : 4;
     static constexpr int MAX_STAGES = 8;                // per warp
     static constexpr int OROW = D + 4;                  // floats per row of the merge buffer (banks)
@@ -77,23 +81,28 @@ __host__ __device__ int tail_bytes(int B, int r, int rd) {
     return QdCfg<D>::OFF_OBUF + obuf_bytes<D>(r, rd) + 4 * (2 * B + 1);
 }
 
-__device__ __forceinline__ int seq_tiles(int L, int Lmax) { return (L >= 1 && L <= Lmax) ? (L + BT - 1) / BT : 0; }
+template <int D>
+__device__ __forceinline__ int seq_tiles(int L, int Lmax) {
+    return (L >= 1 && L <= Lmax) ? (L + QdCfg<D>::BT - 1) / QdCfg<D>::BT : 0;
+}
 
 // Work units of one KV head of a sequence: its tiles and, ahead of them, kPieceTiles that
 // stand for the piece itself.
+template <int D>
 __device__ __forceinline__ int seq_units(int L, int Lmax) {
-    const int n = seq_tiles(L, Lmax);
+    const int n = seq_tiles<D>(L, Lmax);
     return n ? n + kPieceTiles : 0;
 }
 
 // Exclusive prefix of the sequences' units into pb[0..B], and their lengths; all threads.
+template <int D>
 __device__ void unit_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, int* lens, int* red) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int carry = 0;
     for (int base = 0; base < B; base += THREADS) {
         const int i = base + tid;
         const int L = i < B ? seqlens[i] : 0;
-        int v = seq_units(L, Lmax);
+        int v = seq_units<D>(L, Lmax);
         if (i < B) lens[i] = L;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     if (threadIdx.x == 0) *abort_flag = 0;
     // rows of heads that do not exist stay zero
     for (int i = threadIdx.x; i < C::OFF_ML / 4; i += THREADS) reinterpret_cast<uint32_t*>(tail)[i] = 0u;
-    unit_prefix(p.seqlens, p.B, Lmax, pb, lens, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
+    unit_prefix<D>(p.seqlens, p.B, Lmax, pb, lens, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
 
     const int64_t U = (int64_t)p.G * pb[p.B];
     const int N = active_ctas(U, gridDim.x);
@@ -322,40 +331,50 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         fence_proxy_async_global();
     }
 
-    // ---- the warp's copies run n_stages units ahead.  Lane j holds the address of the
-    // warp's block of unit batch + j (0: no tile, or past the sequence's end), 32 table
-    // entries a time.
-    int batch = 0, sent = 0, s_send = 0;
-    uint64_t src = 0;
+    // ---- the warp's copies run n_stages units ahead.  Lane j holds the addresses of the
+    // warp's blocks of unit batch + j (0: no tile, or past the sequence's end), 32 units'
+    // table entries a time, and sends them itself.
+    int sent = 0, s_send = 0;
+    uint64_t src[C::NB] = {};
+    uint32_t has = 0;                  // units of the batch with a block to copy
     uint32_t pending = 0, phases = 0;  // per stage: a copy is under way; parity of its barrier
     auto send = [&]() {  // all lanes; unit `sent` into stage s_send
         if (sent >= n_units) return;
         if ((sent & 31) == 0) {
-            batch = sent;
-            src = 0;
-            if (batch + lane < n_units) {
-                const TileAt t = tile_at(u_begin + batch + lane, pb, p.B, p.G);
-                const int blk = t.i * (BT / kQcBlock) + warp;
-                if (t.i >= 0 && blk * kQcBlock < lens[t.b]) {
-                    int page = p.block_table[(int64_t)t.b * p.max_pages + blk / bpp];
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
-                        page = 0;
+#pragma unroll
+            for (int j = 0; j < C::NB; ++j) src[j] = 0;
+            if (sent + lane < n_units) {
+                const TileAt t = tile_at(u_begin + sent + lane, pb, p.B, p.G);
+#pragma unroll
+                for (int j = 0; j < C::NB; ++j) {
+                    const int blk = (t.i * NW + warp) * C::NB + j;
+                    if (t.i >= 0 && blk * kQcBlock < lens[t.b]) {
+                        int page = p.block_table[(int64_t)t.b * p.max_pages + blk / bpp];
+                        if (page < 0 || page >= p.num_pages) {
+                            atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
+                            page = 0;
+                        }
+                        src[j] = reinterpret_cast<uint64_t>(p.cache + (((int64_t)page * p.G + t.g) * bpp + blk % bpp) * C::BLOCK_BYTES);
                     }
-                    src = reinterpret_cast<uint64_t>(p.cache + (((int64_t)page * p.G + t.g) * bpp + blk % bpp) * C::BLOCK_BYTES);
                 }
             }
+            has = __ballot_sync(0xffffffffu, src[0] != 0);
         }
-        const uint64_t a = __shfl_sync(0xffffffffu, src, sent - batch);
-        if (a) {
-            if (lane == 0) {
-                const uint32_t bar = bars + 8 * s_send, dst = smem_u32(ring + s_send * C::STAGE_BYTES);
-                mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
-                bulk_load(dst, reinterpret_cast<const uint8_t*>(a), C::BLOCK_BYTES, bar);
-                bulk_load(dst + C::BLOCK_BYTES, reinterpret_cast<const uint8_t*>(a) + plane, C::BLOCK_BYTES, bar);
+        if (lane == (sent & 31) && src[0]) {
+            const uint32_t bar = bars + 8 * s_send, dst = smem_u32(ring + s_send * C::STAGE_BYTES);
+            const uint8_t* a = reinterpret_cast<const uint8_t*>(src[0]);
+            const bool two = C::NB == 2 && src[C::NB - 1], joined = two && src[C::NB - 1] == src[0] + C::BLOCK_BYTES;
+            const uint32_t bytes = joined ? 2 * C::BLOCK_BYTES : C::BLOCK_BYTES;
+            mbar_arrive_expect_tx(bar, two ? 4 * C::BLOCK_BYTES : 2 * C::BLOCK_BYTES);
+            bulk_load(dst, a, bytes, bar);
+            bulk_load(dst + C::NB * C::BLOCK_BYTES, a + plane, bytes, bar);
+            if (two && !joined) {
+                const uint8_t* b = reinterpret_cast<const uint8_t*>(src[C::NB - 1]);
+                bulk_load(dst + C::BLOCK_BYTES, b, C::BLOCK_BYTES, bar);
+                bulk_load(dst + (C::NB + 1) * C::BLOCK_BYTES, b + plane, C::BLOCK_BYTES, bar);
             }
-            pending |= 1u << s_send;
         }
+        pending |= (has >> (sent & 31) & 1u) << s_send;
         ++sent;
         if (++s_send == n_stages) s_send = 0;
     };
@@ -396,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
         for (int i = i0; i < i1; ++i) {
-            const int key0 = i * BT + 16 * warp;
+            const int key0 = (i * NW + warp) * C::NB * kQcBlock;
             if (pending >> st & 1u) {
                 if (!dead && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, phases >> st & 1u, abort_flag, p.status)))
                     dead = true;  // keep walking: the block's barriers need every warp
@@ -406,61 +425,82 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                 }
             }
             if (!dead && key0 < L) {
+                constexpr int NB = C::NB, BB = C::BLOCK_BYTES;
                 uint8_t* kb = ring + st * C::STAGE_BYTES;
-                uint8_t* vb = kb + C::BLOCK_BYTES;
-                if (key0 + 16 > L) {  // rows past the end may hold anything: no scale, no centre
-                    uint16_t* par = reinterpret_cast<uint16_t*>(vb + 8 * D);
-                    for (int j = lane; j < 2 * C::NG * 16; j += 32)
-                        if (key0 + (j & 15) >= L) par[j] = 0;
+                uint8_t* vb = kb + NB * BB;
+                if (key0 + NB * kQcBlock > L) {  // rows past the end may hold anything: no scale, no centre
+#pragma unroll
+                    for (int n2 = 0; n2 < NB; ++n2) {
+                        uint16_t* par = reinterpret_cast<uint16_t*>(vb + n2 * BB + 8 * D);
+                        for (int j = lane; j < 2 * C::NG * 16; j += 32)
+                            if (key0 + n2 * kQcBlock + (j & 15) >= L) par[j] = 0;
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                // ---- S^T = K Q^T: lane holds keys gid and gid + 8, heads 2t and 2t + 1
+                // ---- S^T = K Q^T: lane holds keys gid and gid + 8 of each block, heads 2t and 2t + 1
                 const uint8_t* kc = kb + gid * 32 + t * 8;
                 const uint8_t* kp = kb + 8 * D + gid * 2;
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-                {
+                float s[NB][4];
+#pragma unroll
+                for (int n2 = 0; n2 < NB; ++n2) {
                     uint32_t ca = 0, cb = 0;  // centres of groups 2t, 2t + 1
                     if (2 * t < C::NG) {
-                        const uint8_t* c = kb + 9 * D + t * 64 + gid * 2;
+                        const uint8_t* c = kb + n2 * BB + 9 * D + t * 64 + gid * 2;
                         ca = ld<uint16_t>(c) | ((uint32_t)ld<uint16_t>(c + 32) << 16);
                         cb = ld<uint16_t>(c + 16) | ((uint32_t)ld<uint16_t>(c + 48) << 16);
                     }
-                    mma_bf16_16816(s, ca, cb, ca, cb, qhi, qlo);
+                    s[n2][0] = s[n2][1] = s[n2][2] = s[n2][3] = 0.f;
+                    mma_bf16_16816(s[n2], ca, cb, ca, cb, qhi, qlo);
                 }
 #pragma unroll
                 for (int sl = 0; sl < D / 64; ++sl) {
-                    const uint2 wa = ld<uint2>(kc + sl * 512), wb = ld<uint2>(kc + sl * 512 + 256);
+                    uint2 wa[NB], wb[NB];
+#pragma unroll
+                    for (int n2 = 0; n2 < NB; ++n2) {
+                        wa[n2] = ld<uint2>(kc + n2 * BB + sl * 512);
+                        wb[n2] = ld<uint2>(kc + n2 * BB + sl * 512 + 256);
+                    }
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         const int grp = 2 * sl + hf;
                         const uint4 qf = ld<uint4>(qfp + grp * 512);
                         const float4 ci = ld<float4>(cip + grp * 64);
                         const uint32_t sel = hf ? 0x7632 : 0x5410;
-                        const uint32_t c0 = __byte_perm(wa.x, wa.y, sel), c1 = __byte_perm(wb.x, wb.y, sel);
-                        const uint32_t d0 = c0 >> 8, d1 = c1 >> 8;
-                        float a[4];
-                        mma_f16_16816(a, and_or<0x000F000Fu>(c0, one_f16), and_or<0x000F000Fu>(c1, one_f16),
-                                      and_or<0x00F000F0u>(c0, one_f16), and_or<0x00F000F0u>(c1, one_f16), qf.x, qf.y,
-                                      ci.x, ci.y, ci.z, ci.w);
-                        mma_f16_16816(a, and_or<0x000F000Fu>(d0, one_f16), and_or<0x000F000Fu>(d1, one_f16),
-                                      and_or<0x00F000F0u>(d0, one_f16), and_or<0x00F000F0u>(d1, one_f16), qf.z, qf.w,
-                                      a[0], a[1], a[2], a[3]);
-                        const float s0 = __uint_as_float((uint32_t)ld<uint16_t>(kp + grp * 32) << 16);
-                        const float s1 = __uint_as_float((uint32_t)ld<uint16_t>(kp + grp * 32 + 16) << 16);
-                        s[0] = fmaf(s0, a[0], s[0]);
-                        s[1] = fmaf(s0, a[1], s[1]);
-                        s[2] = fmaf(s1, a[2], s[2]);
-                        s[3] = fmaf(s1, a[3], s[3]);
+#pragma unroll
+                        for (int n2 = 0; n2 < NB; ++n2) {
+                            const uint32_t c0 = __byte_perm(wa[n2].x, wa[n2].y, sel), c1 = __byte_perm(wb[n2].x, wb[n2].y, sel);
+                            const uint32_t d0 = c0 >> 8, d1 = c1 >> 8;
+                            float a[4];
+                            mma_f16_16816(a, and_or<0x000F000Fu>(c0, one_f16), and_or<0x000F000Fu>(c1, one_f16),
+                                          and_or<0x00F000F0u>(c0, one_f16), and_or<0x00F000F0u>(c1, one_f16), qf.x, qf.y,
+                                          ci.x, ci.y, ci.z, ci.w);
+                            mma_f16_16816(a, and_or<0x000F000Fu>(d0, one_f16), and_or<0x000F000Fu>(d1, one_f16),
+                                          and_or<0x00F000F0u>(d0, one_f16), and_or<0x00F000F0u>(d1, one_f16), qf.z, qf.w,
+                                          a[0], a[1], a[2], a[3]);
+                            const uint8_t* kpn = kp + n2 * BB + grp * 32;
+                            const float s0 = __uint_as_float((uint32_t)ld<uint16_t>(kpn) << 16);
+                            const float s1 = __uint_as_float((uint32_t)ld<uint16_t>(kpn + 16) << 16);
+                            s[n2][0] = fmaf(s0, a[0], s[n2][0]);
+                            s[n2][1] = fmaf(s0, a[1], s[n2][1]);
+                            s[n2][2] = fmaf(s1, a[2], s[n2][2]);
+                            s[n2][3] = fmaf(s1, a[3], s[n2][3]);
+                        }
                     }
                 }
-                const bool live0 = key0 + gid < L, live1 = key0 + gid + 8 < L;
-                s[0] = live0 ? s[0] * qsc.x : -INFINITY;
-                s[1] = live0 ? s[1] * qsc.y : -INFINITY;
-                s[2] = live1 ? s[2] * qsc.x : -INFINITY;
-                s[3] = live1 ? s[3] * qsc.y : -INFINITY;
+                float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                for (int n2 = 0; n2 < NB; ++n2) {
+                    const int key = key0 + n2 * kQcBlock + gid;
+                    const bool live0 = key < L, live1 = key + 8 < L;
+                    s[n2][0] = live0 ? s[n2][0] * qsc.x : -INFINITY;
+                    s[n2][1] = live0 ? s[n2][1] * qsc.y : -INFINITY;
+                    s[n2][2] = live1 ? s[n2][2] * qsc.x : -INFINITY;
+                    s[n2][3] = live1 ? s[n2][3] * qsc.y : -INFINITY;
+                    t0 = fmaxf(t0, fmaxf(s[n2][0], s[n2][2]));
+                    t1 = fmaxf(t1, fmaxf(s[n2][1], s[n2][3]));
+                }
                 // ---- online softmax; the reference moves only when some logit is 2^8 above it
-                float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
                 if (__any_sync(0xffffffffu, t0 > m_run[0] + 8.f || t1 > m_run[1] + 8.f)) {
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
@@ -485,23 +525,27 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     cacc[0] *= a0;
                     cacc[1] *= a1;
                 }
-                uint32_t pr[2];
+                uint32_t pr[NB][2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t w = pack_bf16x2(ex2_approx(s[2 * k] - m_run[0]), ex2_approx(s[2 * k + 1] - m_run[1]));
-                    l_run[0] += bf16_lo(w);  // the sum of the weights as they are used
-                    l_run[1] += bf16_hi(w);
-                    pr[k] = transpose8x8(w);  // head gid, keys 8k + 2t, 8k + 2t + 1
-                }
+                for (int n2 = 0; n2 < NB; ++n2)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w =
+                            pack_bf16x2(ex2_approx(s[n2][2 * k] - m_run[0]), ex2_approx(s[n2][2 * k + 1] - m_run[1]));
+                        l_run[0] += bf16_lo(w);  // the sum of the weights as they are used
+                        l_run[1] += bf16_hi(w);
+                        pr[n2][k] = transpose8x8(w);  // head gid, keys 8k + 2t, 8k + 2t + 1
+                    }
                 // ---- centres: row g of A is group g
-                {
-                    const uint8_t* ca = vb + 9 * D + gid * 32 + t * 4;
+#pragma unroll
+                for (int n2 = 0; n2 < NB; ++n2) {
+                    const uint8_t* ca = vb + n2 * BB + 9 * D + gid * 32 + t * 4;
                     uint32_t a0 = 0, a2 = 0;
                     if (gid < C::NG) {
                         a0 = ld<uint32_t>(ca);
                         a2 = ld<uint32_t>(ca + 16);
                     }
-                    mma_bf16_16816(cacc, a0, 0u, a2, 0u, pr[0], pr[1]);
+                    mma_bf16_16816(cacc, a0, 0u, a2, 0u, pr[n2][0], pr[n2][1]);
                 }
                 // ---- O^T += V^T P^T
                 const uint8_t* vf = vb + gid * 4 + kf * 32;
@@ -509,25 +553,30 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                 const uint8_t* vp = vb + 8 * D + t * 4;
 #pragma unroll
                 for (int sl = 0; sl < D / 64; ++sl) {
-                    const uint32_t f0 = ld<uint32_t>(vf + sl * 512), s0 = ld<uint32_t>(vs + sl * 512);
-                    const uint32_t f1 = ld<uint32_t>(vf + sl * 512 + 256), s1 = ld<uint32_t>(vs + sl * 512 + 256);
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int grp = 2 * sl + hf;
-                        const uint32_t sel = hf ? sel_hi : sel_lo;
-                        const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
-                        const uint32_t p0 = mul_bf16x2(pr[0], ld<uint32_t>(vp + grp * 32));
-                        const uint32_t p1 = mul_bf16x2(pr[1], ld<uint32_t>(vp + grp * 32 + 16));
+                    for (int n2 = 0; n2 < NB; ++n2) {
+                        const int off = n2 * BB + sl * 512;
+                        const uint32_t f0 = ld<uint32_t>(vf + off), s0 = ld<uint32_t>(vs + off);
+                        const uint32_t f1 = ld<uint32_t>(vf + off + 256), s1 = ld<uint32_t>(vs + off + 256);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            uint32_t a[4];
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int grp = 2 * sl + hf;
+                            const uint32_t sel = hf ? sel_hi : sel_lo;
+                            const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
+                            const uint8_t* vpn = vp + n2 * BB + grp * 32;
+                            const uint32_t p0 = mul_bf16x2(pr[n2][0], ld<uint32_t>(vpn));
+                            const uint32_t p1 = mul_bf16x2(pr[n2][1], ld<uint32_t>(vpn + 16));
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int sh = 4 * (2 * m + k);
-                                a[k] = sub_bf16x2(and_or<0x000F000Fu>(w0 >> sh, one_bf16), kMid);
-                                a[2 + k] = sub_bf16x2(and_or<0x000F000Fu>(w1 >> sh, one_bf16), kMid);
+                            for (int m = 0; m < 2; ++m) {
+                                uint32_t a[4];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int sh = 4 * (2 * m + k);
+                                    a[k] = sub_bf16x2(and_or<0x000F000Fu>(w0 >> sh, one_bf16), kMid);
+                                    a[2 + k] = sub_bf16x2(and_or<0x000F000Fu>(w1 >> sh, one_bf16), kMid);
+                                }
+                                mma_bf16_16816(oacc[2 * grp + m], a[0], a[1], a[2], a[3], p0, p1);
                             }
-                            mma_bf16_16816(oacc[2 * grp + m], a[0], a[1], a[2], a[3], p0, p1);
                         }
                     }
                 }
@@ -634,7 +683,7 @@ __global__ void __launch_bounds__(256) qdecode_combine_kernel(const __grid_const
     __shared__ float sm[8][2], so[8][D];
     const int b = blockIdx.x / p.G, g = blockIdx.x % p.G, r = p.H / p.G, Lmax = p.max_pages * p.page_size;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int L = p.seqlens[b], nt = seq_tiles(L, Lmax);
+    const int L = p.seqlens[b], nt = seq_tiles<D>(L, Lmax);
     // every block waits for the split kernel before it leaves: this grid's end then means both
     if (L == 0) {
         pdl_wait_prerequisites();
@@ -650,7 +699,7 @@ __global__ void __launch_bounds__(256) qdecode_combine_kernel(const __grid_const
     }
     int before = 0, total = 0;  // units ahead of this sequence, and of all
     for (int i = lane; i < p.B; i += 32) {
-        const int n = seq_units(p.seqlens[i], Lmax);
+        const int n = seq_units<D>(p.seqlens[i], Lmax);
         total += n;
         if (i < b) before += n;
     }
