@@ -173,6 +173,15 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
     asm volatile("" : "+r"(x));
     return x;
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 template <typename T>
 __device__ __forceinline__ T ld(const uint8_t* p) {
     return *reinterpret_cast<const T*>(p);
@@ -305,6 +314,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     const int r = p.H / p.G, Lmax = p.max_pages * p.page_size;
     int* pb = reinterpret_cast<int*>(tail + C::OFF_OBUF + obuf_bytes<D>(r, p.rd));
     int* lens = pb + p.B + 1;
+    const uint32_t ring_u32 = smem_u32(smem) + warp * n_stages * C::STAGE_BYTES;
     uint8_t* ring = smem + warp * n_stages * C::STAGE_BYTES;
     const uint32_t bars = smem_u32(tail + C::OFF_BAR) + warp * 8 * C::MAX_STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
@@ -332,12 +342,11 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     }
 
     // ---- the warp's copies run n_stages units ahead.  Lane j holds the addresses of the
-    // warp's blocks of unit batch + j (0: no tile, or past the sequence's end), 32 units'
-    // table entries a time, and sends them itself.
+    // warp's blocks of unit 32 k + j (0: no tile, or past the sequence's end), 32 units'
+    // table entries a time.  A unit without a block still completes its stage's phase, so
+    // the stages' parities flip together.
     int sent = 0, s_send = 0;
     uint64_t src[C::NB] = {};
-    uint32_t has = 0;                  // units of the batch with a block to copy
-    uint32_t pending = 0, phases = 0;  // per stage: a copy is under way; parity of its barrier
     auto send = [&]() {  // all lanes; unit `sent` into stage s_send
         if (sent >= n_units) return;
         if ((sent & 31) == 0) {
@@ -358,23 +367,32 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     }
                 }
             }
-            has = __ballot_sync(0xffffffffu, src[0] != 0);
         }
-        if (lane == (sent & 31) && src[0]) {
-            const uint32_t bar = bars + 8 * s_send, dst = smem_u32(ring + s_send * C::STAGE_BYTES);
-            const uint8_t* a = reinterpret_cast<const uint8_t*>(src[0]);
-            const bool two = C::NB == 2 && src[C::NB - 1], joined = two && src[C::NB - 1] == src[0] + C::BLOCK_BYTES;
-            const uint32_t bytes = joined ? 2 * C::BLOCK_BYTES : C::BLOCK_BYTES;
-            mbar_arrive_expect_tx(bar, two ? 4 * C::BLOCK_BYTES : 2 * C::BLOCK_BYTES);
-            bulk_load(dst, a, bytes, bar);
-            bulk_load(dst + C::NB * C::BLOCK_BYTES, a + plane, bytes, bar);
-            if (two && !joined) {
-                const uint8_t* b = reinterpret_cast<const uint8_t*>(src[C::NB - 1]);
-                bulk_load(dst + C::BLOCK_BYTES, b, C::BLOCK_BYTES, bar);
-                bulk_load(dst + (C::NB + 1) * C::BLOCK_BYTES, b + plane, C::BLOCK_BYTES, bar);
+        uint64_t a[C::NB];
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j) a[j] = __shfl_sync(0xffffffffu, src[j], sent & 31);
+        if (elect_one()) {
+            const uint32_t bar = bars + 8 * s_send, dst = ring_u32 + s_send * C::STAGE_BYTES;
+            const uint8_t* k0 = reinterpret_cast<const uint8_t*>(a[0]);
+            if (C::NB == 2 && a[C::NB - 1] == a[0] + C::BLOCK_BYTES) {  // two blocks in a row
+                mbar_arrive_expect_tx(bar, 4 * C::BLOCK_BYTES);
+                bulk_load(dst, k0, 2 * C::BLOCK_BYTES, bar);
+                bulk_load(dst + 2 * C::BLOCK_BYTES, k0 + plane, 2 * C::BLOCK_BYTES, bar);
+            } else if (a[0]) {
+                const bool two = C::NB == 2 && a[C::NB - 1];
+                mbar_arrive_expect_tx(bar, (two ? 4 : 2) * C::BLOCK_BYTES);
+                bulk_load(dst, k0, C::BLOCK_BYTES, bar);
+                bulk_load(dst + C::NB * C::BLOCK_BYTES, k0 + plane, C::BLOCK_BYTES, bar);
+                if (two) {
+                    const uint8_t* k1 = reinterpret_cast<const uint8_t*>(a[C::NB - 1]);
+                    bulk_load(dst + C::BLOCK_BYTES, k1, C::BLOCK_BYTES, bar);
+                    bulk_load(dst + (C::NB + 1) * C::BLOCK_BYTES, k1 + plane, C::BLOCK_BYTES, bar);
+                }
+            } else {
+                mbar_arrive(bar);
             }
         }
-        pending |= (has >> (sent & 31) & 1u) << s_send;
+        __syncwarp();
         ++sent;
         if (++s_send == n_stages) s_send = 0;
     };
@@ -387,8 +405,24 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     const uint32_t sel_lo = t < 2 ? 0x5410u : 0x1054u, sel_hi = t < 2 ? 0x7632u : 0x3276u;
     const uint32_t one_f16 = opaque(0x64006400u), one_bf16 = opaque(0x43004300u);  // 1024, 128
     constexpr uint32_t kMid = 0x43084308u;                                         // 136
-    int st = 0;
+    int st = 0, done = 0;  // stage and number of the unit at hand
+    uint32_t phase = 0;
     bool dead = false;
+    // waits for the unit at hand; a wait that runs out leaves the warp walking on without data,
+    // because the block's barriers need every warp
+    auto receive = [&]() {
+        if (!dead && !__all_sync(0xffffffffu, mbar_try_wait(bars + 8 * st, phase)))
+            dead = !__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, phase, abort_flag, p.status));
+        done += !dead;
+    };
+    auto release = [&]() {  // the warp is through with the stage: the next copy goes there
+        __syncwarp();
+        if (!dead) send();
+        if (++st == n_stages) {
+            st = 0;
+            phase ^= 1u;
+        }
+    };
     TileAt at = tile_at(u_begin, pb, p.B, p.G);
     for (int n = 0; n < n_units;) {
         const int i1 = min(at.nt, at.i + (n_units - n));  // this CTA's tiles of the piece: [i0, i1)
@@ -396,8 +430,8 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         const int L = lens[at.b];
         n += i1 - at.i;
         for (int i = at.i; i < min(i0, i1); ++i) {  // the piece's own units hold no tile
-            send();
-            if (++st == n_stages) st = 0;
+            receive();
+            release();
         }
         if (i1 <= 0) break;
         const bool alone = i0 == 0 && i1 == at.nt;
@@ -416,19 +450,13 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 
         for (int i = i0; i < i1; ++i) {
             const int key0 = (i * NW + warp) * C::NB * kQcBlock;
-            if (pending >> st & 1u) {
-                if (!dead && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, phases >> st & 1u, abort_flag, p.status)))
-                    dead = true;  // keep walking: the block's barriers need every warp
-                if (!dead) {
-                    pending &= ~(1u << st);
-                    phases ^= 1u << st;
-                }
-            }
+            receive();
             if (!dead && key0 < L) {
                 constexpr int NB = C::NB, BB = C::BLOCK_BYTES;
                 uint8_t* kb = ring + st * C::STAGE_BYTES;
                 uint8_t* vb = kb + NB * BB;
-                if (key0 + NB * kQcBlock > L) {  // rows past the end may hold anything: no scale, no centre
+                const bool ragged = key0 + NB * kQcBlock > L;
+                if (ragged) {  // rows past the end may hold anything: no scale, no centre
 #pragma unroll
                     for (int n2 = 0; n2 < NB; ++n2) {
                         uint16_t* par = reinterpret_cast<uint16_t*>(vb + n2 * BB + 8 * D);
@@ -491,12 +519,15 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                 for (int n2 = 0; n2 < NB; ++n2) {
-                    const int key = key0 + n2 * kQcBlock + gid;
-                    const bool live0 = key < L, live1 = key + 8 < L;
-                    s[n2][0] = live0 ? s[n2][0] * qsc.x : -INFINITY;
-                    s[n2][1] = live0 ? s[n2][1] * qsc.y : -INFINITY;
-                    s[n2][2] = live1 ? s[n2][2] * qsc.x : -INFINITY;
-                    s[n2][3] = live1 ? s[n2][3] * qsc.y : -INFINITY;
+                    s[n2][0] *= qsc.x;
+                    s[n2][1] *= qsc.y;
+                    s[n2][2] *= qsc.x;
+                    s[n2][3] *= qsc.y;
+                    if (ragged) {
+                        const int key = key0 + n2 * kQcBlock + gid;
+                        if (key >= L) s[n2][0] = s[n2][1] = -INFINITY;
+                        if (key + 8 >= L) s[n2][2] = s[n2][3] = -INFINITY;
+                    }
                     t0 = fmaxf(t0, fmaxf(s[n2][0], s[n2][2]));
                     t1 = fmaxf(t1, fmaxf(s[n2][1], s[n2][3]));
                 }
@@ -581,9 +612,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     }
                 }
             }
-            __syncwarp();
-            if (!dead) send();  // into the stage just read
-            if (++st == n_stages) st = 0;
+            release();
         }
 
         // -------- end of the piece: merge the four warps, then finish or hand over
@@ -669,8 +698,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         }
     }
     // every copy that was sent lands before the block leaves (none is left unless a wait ran out)
-    for (int s = 0; s < n_stages; ++s)
-        if (pending >> s & 1u) mbar_wait_drain(bars + 8 * s, phases >> s & 1u, p.status);
+    for (; done < sent; ++done) mbar_wait_drain(bars + 8 * (done % n_stages), (uint32_t)(done / n_stages) & 1u, p.status);
 }
 
 // Merge the partial states of one (sequence, KV head) that several CTAs share and apply
