@@ -31,7 +31,7 @@ __device__ __forceinline__ int64_t qc_block_offset(int page, int g, int slot, in
     return (((int64_t)page * G + g) * (page_size / kQcBlock) + slot / kQcBlock) * qc_block_bytes(d);
 }
 
-// max / min that return NaN when either side is one
+// max / min that return NaN when any operand is one
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -40,6 +40,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -67,17 +77,27 @@ __device__ __forceinline__ QcGroup qc_group(float lo, float hi) {
 
 // Eight codes of one group as nibbles, lowest feature first.  Adding 1.5 * 2^23 rounds
 // the product to an integer half to even in one rounding and leaves code - 8 in the low
-// mantissa bits (two's complement); flipping bit 3 of each nibble adds the 8.
-__device__ __forceinline__ uint32_t qc_encode8(const float (&x)[8], const QcGroup& q) {
-    constexpr float kMagic = 12582912.f;
-    uint32_t w = 0;
+// mantissa bits (two's complement); flipping bit 3 of each nibble adds the 8.  CLAMP is
+// needed only where a group's own extremes fall outside [-8, 7] (the codes are monotonic
+// in x), which takes a centre so large that its rounding is half a step.
+constexpr float kQcMagic = 12582912.f;
+__device__ __forceinline__ float qc_round(float x, const QcGroup& q) {
+    return fmaf(__fsub_rn(x, q.centre), q.inv, kQcMagic);
+}
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t qc_encode8(const float* x, const QcGroup& q) {
+    uint32_t b[4];  // byte i: features 2i (low nibble) and 2i + 1; garbage above it
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = fmaf(__fsub_rn(x[i], q.centre), q.inv, kMagic);
-        const float u = fminf(fmaxf(t, kMagic - 8.f), kMagic + 7.f);
-        w |= (__float_as_uint(u) & 15u) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+        float t0 = qc_round(x[2 * i], q), t1 = qc_round(x[2 * i + 1], q);
+        if (CLAMP) {
+            t0 = fminf(fmaxf(t0, kQcMagic - 8.f), kQcMagic + 7.f);
+            t1 = fminf(fmaxf(t1, kQcMagic - 8.f), kQcMagic + 7.f);
+        }
+        const uint32_t hi = __float_as_uint(t1) << 4;
+        b[i] = (__float_as_uint(t0) & 15u) | (hi & ~15u);
     }
-    return w ^ 0x88888888u;
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^ 0x88888888u;
 }
 
 // sin and cos of the RoPE angle pos * f, f in 2^-64 turns: the product modulo one turn is

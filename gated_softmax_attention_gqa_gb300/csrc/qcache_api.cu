@@ -79,7 +79,7 @@ gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, cons
     if (!seqlens || !knorm_w || !aligned(seqlens, 4) || !aligned(cu_seqlens, 4) || !aligned(knorm_w, 16))
         return GATTN_ERR_INVALID_ARG;
     if (T == 0) return GATTN_OK;
-    if (!k || !v || (int64_t)T * G > (int64_t)INT32_MAX) return GATTN_ERR_INVALID_ARG;
+    if (!k || !v || (int64_t)T * G > ((int64_t)1 << 30)) return GATTN_ERR_INVALID_ARG;
     if (k_tok_stride == 0) k_tok_stride = (int64_t)G * d;
     if (k_head_stride == 0) k_head_stride = d;
     if (v_tok_stride == 0) v_tok_stride = (int64_t)G * d;
@@ -125,7 +125,7 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
     if (st != GATTN_OK) return st;
     if (!aligned(starts, 4) || !aligned(cu_seqlens, 4)) return GATTN_ERR_INVALID_ARG;
     if (T == 0) return GATTN_OK;
-    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || (int64_t)T * G > (int64_t)INT32_MAX)
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || (int64_t)T * G > ((int64_t)1 << 30))
         return GATTN_ERR_INVALID_ARG;
     QcacheReadParams p;
     std::memset(&p, 0, sizeof(p));
