@@ -254,7 +254,7 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
         }
 #pragma unroll
         for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rinv = 1.0f / sqrtf(ss / (float)D + p.eps);
+        const float rinv = inv_sqrt(ss / (float)D + p.eps);
         const bool rot = e0 < p.rd, first = e0 < half;
         const int src = rot ? lane + (first ? half >> 3 : -(half >> 3)) : lane;
         float big = 0.f;

@@ -143,6 +143,11 @@ gattn_status decode_check_args(const void* q_new, const void* kv_cache, const in
                                const void* qnorm_w, int B, int H, int G, int d, int Lmax, int rotary_dim,
                                double rope_base, float eps, int gate_mode, const void* out, int64_t cache_rows);
 
+// Division by page_size of a token index below 2^31: (x * mul) >> 32 >> shift.
+struct PageDiv {
+    uint32_t mul, shift;
+};
+
 // 4-bit KV cache (qcache.cuh).  turns[i]: rotation of pair i per position, in 2^-64 turns.
 struct QcacheWriteParams {
     const void* k;
@@ -154,6 +159,7 @@ struct QcacheWriteParams {
     const void* knorm_w;
     int64_t k_tok_stride, k_head_stride, v_tok_stride, v_head_stride;
     int num_pages, page_size, max_pages;
+    PageDiv by_page;
     int T, B, G, d, rd;
     float eps;
     unsigned int* status;
@@ -167,6 +173,7 @@ struct QcacheReadParams {
     void* k;
     void* v;
     int num_pages, page_size, max_pages;
+    PageDiv by_page;
     int T, B, G, d;
     unsigned int* status;
 };

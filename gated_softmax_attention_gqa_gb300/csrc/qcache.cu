@@ -4,9 +4,11 @@
 // number and leaves 0.625, the read the reverse, so HBM bounds both as long as the
 // arithmetic stays small: at 6.8 TB/s an SM has some 14 instruction slots for a written
 // number.  So a lane takes 16 features (half a scale group) of one token and walks its KV
-// heads: the token's place, its sines and cosines (made once per warp, in shared memory)
-// and their products with the norm weights are shared by all heads, and what a group
-// costs (extremes, scale, reciprocal) is shared by 32 numbers and two lanes.
+// heads: the token's sines and cosines (made once per warp, in shared memory) and their
+// products with the norm weights are shared by all heads, and what a group costs
+// (extremes, scale, reciprocal) is shared by 32 numbers and two lanes.  The chain of
+// lookups that finds a token's row (sequence, length, page) is walked by one lane per
+// token for all the tokens a warp will deal with.
 #include "qcache.cuh"
 
 namespace gattn {
@@ -20,6 +22,7 @@ struct Row16;
 template <>
 struct Row16<bf16> {
     uint4 v[2];
+    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const bf16* p) {
         v[0] = reinterpret_cast<const uint4*>(p)[0];
         v[1] = reinterpret_cast<const uint4*>(p)[1];
@@ -41,6 +44,7 @@ struct Row16<bf16> {
 template <>
 struct Row16<float> {
     float4 v[4];
+    __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = v[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
@@ -65,14 +69,18 @@ struct Row16<float> {
 struct Place {
     int pos, page, slot;
 };
+__device__ __forceinline__ Place place_of(const Place& at, int lane) {
+    return Place{__shfl_sync(0xffffffffu, at.pos, lane), __shfl_sync(0xffffffffu, at.page, lane),
+                 __shfl_sync(0xffffffffu, at.slot, lane)};
+}
 enum { kSkip = 0, kLive = 1, kBadLength = 2, kBadPage = 3 };
 
-__device__ __forceinline__ int find_page(const int32_t* table, int max_pages, int num_pages, int page_size, int b,
-                                         Place& at) {
-    const int k = at.pos / page_size;
-    at.slot = at.pos - k * page_size;
-    at.page = table[(int64_t)b * max_pages + k];
-    return at.page >= 0 && at.page < num_pages ? kLive : kBadPage;
+template <typename P>
+__device__ __forceinline__ int find_page(const P& p, int b, Place& at) {
+    const int k = (int)(__umulhi((uint32_t)at.pos, p.by_page.mul) >> p.by_page.shift);
+    at.slot = at.pos - k * p.page_size;
+    at.page = p.block_table[(int64_t)b * p.max_pages + k];
+    return at.page >= 0 && at.page < p.num_pages ? kLive : kBadPage;
 }
 
 __device__ __forceinline__ int place_new(const QcacheWriteParams& p, int t, Place& at) {
@@ -91,7 +99,7 @@ __device__ __forceinline__ int place_new(const QcacheWriteParams& p, int t, Plac
     if (!p.cu_seqlens && L == 0) return kSkip;
     if (L > p.max_pages * p.page_size || L < n) return kBadLength;
     at.pos = L - n + j;
-    return find_page(p.block_table, p.max_pages, p.num_pages, p.page_size, b, at);
+    return find_page(p, b, at);
 }
 
 __device__ __forceinline__ int place_cached(const QcacheReadParams& p, int t, Place& at) {
@@ -108,7 +116,7 @@ __device__ __forceinline__ int place_cached(const QcacheReadParams& p, int t, Pl
     const int64_t start = p.starts ? p.starts[b] : 0;
     if (start < 0 || start + n > (int64_t)p.max_pages * p.page_size) return kBadLength;
     at.pos = (int)start + j;
-    return find_page(p.block_table, p.max_pages, p.num_pages, p.page_size, b, at);
+    return find_page(p, b, at);
 }
 
 __device__ __forceinline__ bool report(int what, unsigned int* status) {
@@ -148,196 +156,232 @@ __device__ __forceinline__ void encode_store(const float (&x)[16], uint8_t* bloc
         make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     // the group's two lanes store its scale and its centre
     reinterpret_cast<uint16_t*>(block + 8 * d)[j * (d / 2) + (e0 >> 5) * 16 + row] =
-        (uint16_t)(j ? q.centre_bits : q.scale_bits);
+        (uint16_t)(j ? q.bits >> 16 : q.bits);
 }
 
-// A token is spread over D / 16 lanes; a warp takes 32 / (D / 16) neighbouring tokens and
-// walks heads [blockIdx.y heads, ...).
+// A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass of a warp; a warp
+// takes `passes` of them and walks heads [blockIdx.y heads, ...) in each.
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kWarps) qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int heads) {
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
-    __shared__ float2 tables[kWarps][TPW * D / 2];
+    __shared__ __align__(16) float2 tables[kWarps][TPW * D / 2 + 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t0 = (blockIdx.x * kWarps + warp) * TPW;
+    const int t0 = (blockIdx.x * kWarps + warp) * TPW * passes;
     if (t0 >= p.T) return;
-    const int tl = lane / LPR, t = t0 + tl, e0 = 16 * (lane % LPR);
-    const int g0 = blockIdx.y * heads, g1 = min(p.G, g0 + heads);
-    const int64_t row0 = min(t, p.T - 1);
-    const T* kp = static_cast<const T*>(p.k) + row0 * p.k_tok_stride + g0 * p.k_head_stride + e0;
-    const T* vp = static_cast<const T*>(p.v) + row0 * p.v_tok_stride + g0 * p.v_head_stride + e0;
-    // rotation partners, eight features at a time (rotary_dim / 2 is a multiple of 8)
+    const int e0 = 16 * (lane % LPR), g0 = blockIdx.y * heads, n_heads = min(p.G, g0 + heads) - g0;
     const int half = p.rd >> 1;
-    bool rot[2];
-    int mate[2];  // the partners' distance
+    // rotation partners, eight features at a time (half is a multiple of 8); features past
+    // rotary_dim are their own, turned by nothing (entries half .. half + 7 of a table)
+    int mate[2], turn[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        rot[c] = e0 + 8 * c < p.rd;
-        mate[c] = e0 + 8 * c < half ? half : -half;
+        const int e = e0 + 8 * c;
+        mate[c] = e < half ? half : e < p.rd ? -half : 0;
+        turn[c] = e < half ? e : e - half;
     }
+    const T* kp;
+    const T* vp;
     Row16<T> kr, ko, vr;
+    auto start = [&](int pass) {  // the first head's rows of a pass
+        const int64_t t = min(t0 + pass * TPW + lane / LPR, p.T - 1);
+        kp = static_cast<const T*>(p.k) + t * p.k_tok_stride + g0 * p.k_head_stride + e0;
+        vp = static_cast<const T*>(p.v) + t * p.v_tok_stride + g0 * p.v_head_stride + e0;
+    };
     auto load_k = [&]() {
         kr.load(kp);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-            if (rot[c]) ko.load8(c, kp + 8 * c + mate[c]);
+            if (mate[c]) ko.load8(c, kp + 8 * c + mate[c]);
     };
+    start(0);
+    ko.zero();
     load_k();
 
-    Place at;
-    const bool live = report(place_new(p, t, at), p.status);
+    Place mine;  // of token t0 + lane
+    const bool ok = report(lane < passes * TPW ? place_new(p, t0 + lane, mine) : kSkip, p.status);
+    if (!ok) mine = Place{0, -1, 0};
 
-    // sines and cosines of the warp's tokens
-    float2* table = tables[warp];
-    for (int i0 = 0; i0 < TPW * half; i0 += 32) {
-        const int i = i0 + lane, k = min(i / max(half, 1), TPW - 1);
-        const int pos = __shfl_sync(0xffffffffu, at.pos, k * LPR);
-        if (i < TPW * half) {
-            float s, c;
-            rope_turn_sincos(p.turns[i - k * half], pos, &s, &c);
-            table[i] = make_float2(s, c);
-        }
-    }
-    __syncwarp();
-    // K' = (x wc + partner ws) / rms, with the norm weights in wc and ws
-    float wc[16], ws[16];
+    float w[16], m[16];  // norm weights, and the partners' with the rotation's sign
     {
         Row16<T> wr;
-        float w[16];
         wr.load(static_cast<const T*>(p.knorm_w) + e0);
         wr.get(w);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float m[16];
-            const int e = e0 + 8 * c;
-            if (rot[c]) {
-                wr.load8(c, static_cast<const T*>(p.knorm_w) + e + mate[c]);
-                wr.get(m);
-            }
-            const float2* sc = table + tl * half + (e < half ? e : e - half);
+        for (int c = 0; c < 2; ++c) wr.load8(c, static_cast<const T*>(p.knorm_w) + e0 + 8 * c + mate[c]);
+        wr.get(m);
 #pragma unroll
-            for (int i = 8 * c; i < 8 * c + 8; ++i) {
-                wc[i] = w[i];
-                ws[i] = 0.f;
-                if (rot[c]) {
-                    const float2 v = sc[i - 8 * c];
-                    wc[i] = w[i] * v.y;
-                    ws[i] = m[i] * (e < half ? -v.x : v.x);
-                }
-            }
-        }
+        for (int i = 0; i < 16; ++i) m[i] = mate[i >> 3] > 0 ? -m[i] : m[i];
     }
-    const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * qc_block_bytes(D);
-    const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D);
-    uint8_t* block = p.cache + (live ? qc_block_offset(at.page, g0, at.slot, p.G, p.page_size, D) : 0);
-    const int row = live ? at.slot % kQcBlock : 0;
-    const bool any_rot = p.rd > 0;
-    for (int g = g0; g < g1; ++g) {
-        vr.load(vp);
-        float x[16], o[16], ss = 0.f;
-        kr.get(x);
+    float2* table = tables[warp];
+    const float2* sc[2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int c = 0; c < 2; ++c) sc[c] = table + (mate[c] ? (lane / LPR) * half + turn[c] : TPW * half);
+    if (lane < 8) table[TPW * half + lane] = make_float2(0.f, 1.f);
+    const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
+
+    for (int pass = 0; pass < passes; ++pass) {
+        if (t0 + pass * TPW >= p.T) break;
+        // sines and cosines of the pass's tokens
+        __syncwarp();
+        for (int k = 0; k < TPW; ++k) {
+            const int pos = __shfl_sync(0xffffffffu, mine.pos, pass * TPW + k);
+            for (int i = lane; i < half; i += 32) {
+                float s, c;
+                rope_turn_sincos(p.turns[i], pos, &s, &c);
+                table[k * half + i] = make_float2(s, c);
+            }
+        }
+        __syncwarp();
+        // K' = (x wc + partner ws) / rms
+        float wc[16], ws[16];
 #pragma unroll
-        for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-        const float rinv = 1.0f / sqrtf(ss / (float)D + p.eps);
-        if (any_rot) {
+        for (int i = 0; i < 16; i += 2) {
+            const float4 v = *reinterpret_cast<const float4*>(sc[i >> 3] + (i & 7));
+            wc[i] = w[i] * v.y;
+            ws[i] = m[i] * v.x;
+            wc[i + 1] = w[i + 1] * v.w;
+            ws[i + 1] = m[i + 1] * v.z;
+        }
+        const Place at = place_of(mine, pass * TPW + lane / LPR);
+        const bool live = at.page >= 0;
+        uint8_t* block = p.cache + (live ? (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) : 0);
+        const int row = at.slot % kQcBlock;
+        for (int g = 0; g < n_heads; ++g) {
+            vr.load(vp);
+            vp += p.v_head_stride;
+            float x[16], o[16], ss = 0.f;
+            kr.get(x);
             ko.get(o);
+            // the next K rows: the next head's, or the next pass's first
+            if (g + 1 < n_heads) {
+                kp += p.k_head_stride;
+                load_k();
+            } else if (pass + 1 < passes) {
+                start(pass + 1);
+                load_k();
+            }
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-                for (int i = 8 * c; i < 8 * c + 8; ++i) x[i] = fmaf(x[i], wc[i], rot[c] ? o[i] * ws[i] : 0.f) * rinv;
-        } else {
+            for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+            const float rinv = inv_sqrt(ss / (float)D + p.eps);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = x[i] * wc[i] * rinv;
+            for (int i = 0; i < 16; ++i) x[i] = fmaf(x[i], wc[i], o[i] * ws[i]) * rinv;
+            encode_store(x, block, row, e0, D, live);
+            vr.get(x);
+            encode_store(x, block + plane, row, e0, D, live);
+            block += head;
         }
-        if (g + 1 < g1) {
-            kp += p.k_head_stride;
-            load_k();
-        }
-        encode_store(x, block, row, e0, D, live);
-        vr.get(x);
-        encode_store(x, block + plane, row, e0, D, live);
-        vp += p.v_head_stride;
-        block += head;
     }
 }
 
-__device__ __forceinline__ void store8(bf16* p, const float* x) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+// Eight stored features (their nibbles lowest first) as bf16 or fp32.  bf16: a nibble or-ed
+// into 128's mantissa reads as 128 + code; the difference to 136 is exact and the fused
+// multiply-add rounds centre + scale (code - 8) once.
+__device__ __forceinline__ void decode8(uint32_t n, uint32_t s2, uint32_t c2, bf16* out) {
+    uint32_t r[4];  // features i and i + 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t v = ((n >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+        uint32_t u;
+        asm("sub.bf16x2 %0, %1, %2;" : "=r"(u) : "r"(v), "r"(0x43084308u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(u), "r"(s2), "r"(c2));
+    }
+    *reinterpret_cast<uint4*>(out) = make_uint4(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[2], r[3], 0x5410),
+                                                __byte_perm(r[0], r[1], 0x7632), __byte_perm(r[2], r[3], 0x7632));
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void decode8(uint32_t n, uint32_t s2, uint32_t c2, float* out) {
+    const float s = bf16_lo(s2), c = bf16_lo(c2);
+    float x[8];
+    // 2^23 + code as a float; the difference to 2^23 + 8 is exact
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = fmaf(s, __uint_as_float(((n >> (4 * k)) & 15u) | 0x4B000000u) - 8388616.f, c);
+    reinterpret_cast<float4*>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
 // The same layout of work: a lane reads back 16 features of one token, head after head.
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kWarps) qcache_read_kernel(const __grid_constant__ QcacheReadParams p, int heads) {
+__global__ void __launch_bounds__(32 * kWarps)
+    qcache_read_kernel(const __grid_constant__ QcacheReadParams p, int passes, int heads) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t0 = (blockIdx.x * kWarps + warp) * TPW;
+    const int t0 = (blockIdx.x * kWarps + warp) * TPW * passes;
     if (t0 >= p.T) return;
-    const int t = t0 + lane / LPR, e0 = 16 * (lane % LPR);
-    Place at;
-    if (!report(place_cached(p, t, at), p.status)) return;
-    const int g0 = blockIdx.y * heads, n = 2 * (min(p.G, g0 + heads) - g0);
-    const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * qc_block_bytes(D);
-    const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D);
-    const uint8_t* block = p.cache + qc_block_offset(at.page, g0, at.slot, p.G, p.page_size, D);
-    const int row = at.slot % kQcBlock, j = (e0 >> 4) & 1, upper = (e0 >> 5) & 1;
-    const int codes = (e0 >> 6) * 512 + row * 32 + 16 * j, par = 8 * D + ((e0 >> 5) * 16 + row) * 2;
-    T* kout = static_cast<T*>(p.k) + ((int64_t)t * p.G + g0) * D + e0;
-    T* vout = static_cast<T*>(p.v) + ((int64_t)t * p.G + g0) * D + e0;
+    const int e0 = 16 * (lane % LPR), g0 = blockIdx.y * heads, n_heads = min(p.G, g0 + heads) - g0;
+    Place mine;  // of token t0 + lane
+    const bool ok = report(lane < passes * TPW ? place_cached(p, t0 + lane, mine) : kSkip, p.status);
+    if (!ok) mine = Place{0, -1, 0};
+    const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
+    const int j = (e0 >> 4) & 1, upper = (e0 >> 5) & 1;
     const uint32_t sel = upper ? 0x7632 : 0x5410;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {  // K and V of each head in turn
-        const uint8_t* src = block + (i >> 1) * head + (i & 1) * plane;
-        const uint4 w = *reinterpret_cast<const uint4*>(src + codes);
-        const float s = __bfloat162float(*reinterpret_cast<const bf16*>(src + par));
-        const float c = __bfloat162float(*reinterpret_cast<const bf16*>(src + par + D));
-        const uint32_t n8[2] = {__byte_perm(w.x, w.y, sel), __byte_perm(w.z, w.w, sel)};
-        T* out = ((i & 1) ? vout : kout) + (i >> 1) * D;
+    for (int pass = 0; pass < passes; ++pass) {
+        const Place at = place_of(mine, pass * TPW + lane / LPR);
+        if (at.page < 0) continue;  // no lane of this token goes on; the shuffles above are whole again next time
+        const int64_t t = t0 + pass * TPW + lane / LPR;
+        const int row = at.slot % kQcBlock;
+        const uint8_t* src = p.cache + (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) +
+                             (e0 >> 6) * 512 + row * 32 + 16 * j;
+        const int par = 8 * D + ((e0 >> 5) * 16 + row) * 2 - ((e0 >> 6) * 512 + row * 32 + 16 * j);
+        T* kout = static_cast<T*>(p.k) + (t * p.G + g0) * D + e0;
+        T* vout = static_cast<T*>(p.v) + (t * p.G + g0) * D + e0;
+#pragma unroll 2
+        for (int g = 0; g < n_heads; ++g) {
+            uint4 w[2];
+            uint32_t s[2], c[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float x[8];
-            // 2^23 + code as a float; one subtraction leaves code - 8
+            for (int i = 0; i < 2; ++i) {  // K and V
+                w[i] = *reinterpret_cast<const uint4*>(src + i * plane);
+                s[i] = *reinterpret_cast<const uint16_t*>(src + i * plane + par);
+                c[i] = *reinterpret_cast<const uint16_t*>(src + i * plane + par + D);
+            }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                x[k] = fmaf(s, __uint_as_float(((n8[h] >> (4 * k)) & 15u) | 0x4B000000u) - 8388616.f, c);
-            store8(out + 8 * h, x);
+            for (int i = 0; i < 2; ++i) {
+                T* out = i ? vout : kout;
+                const uint32_t s2 = s[i] * 0x10001u, c2 = c[i] * 0x10001u;
+                decode8(__byte_perm(w[i].x, w[i].y, sel), s2, c2, out);
+                decode8(__byte_perm(w[i].z, w[i].w, sel), s2, c2, out + 8);
+            }
+            src += head;
+            kout += D;
+            vout += D;
         }
     }
 }
 
-// Warps walk all heads of their tokens where that gives every SM work; else the heads are
-// spread over the grid's second dimension.  (64 tokens of two heads: 4.2 us in one
-// dimension; 131072 tokens of two: no difference.)
-int heads_per_warp(int64_t token_warps, int G) {
-    int heads = G;
-    while (heads > 1 && token_warps * ((G + heads - 1) / heads) < 8 * device_sm_count()) heads = (heads + 1) / 2;
-    return heads;
-}
-
+// How a call is cut: passes a warp takes (their lookups go together) and KV heads.  Both
+// shrink while they leave the device short of warps, as for a few tokens of a decode step.
+struct Cut {
+    int passes, heads;
+    dim3 grid;
+};
 template <int D>
-dim3 grid_of(int T, int G, int heads) {
-    constexpr int tokens = kWarps * (32 / (D / 16));
-    return dim3((unsigned)((T + tokens - 1) / tokens), (unsigned)((G + heads - 1) / heads));
+Cut cut_of(int T, int G) {
+    constexpr int TPW = 32 / (D / 16);
+    const int64_t want = 16 * (int64_t)device_sm_count();
+    Cut c{4, G, dim3()};
+    auto warps = [&]() { return ((int64_t)T + TPW * c.passes - 1) / (TPW * c.passes) * ((G + c.heads - 1) / c.heads); };
+    while (c.passes > 1 && warps() < want) c.passes /= 2;
+    while (c.heads > 1 && warps() < want) c.heads = (c.heads + 1) / 2;
+    const int tokens = kWarps * TPW * c.passes;
+    c.grid = dim3((unsigned)((T + tokens - 1) / tokens), (unsigned)((G + c.heads - 1) / c.heads));
+    return c;
 }
 
 template <int D>
 cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) {
-    const int heads = heads_per_warp((p.T + 32 / (D / 16) - 1) / (32 / (D / 16)), p.G);
-    if (fp32) qcache_write_kernel<D, float><<<grid_of<D>(p.T, p.G, heads), 32 * kWarps, 0, stream>>>(p, heads);
-    else qcache_write_kernel<D, bf16><<<grid_of<D>(p.T, p.G, heads), 32 * kWarps, 0, stream>>>(p, heads);
+    const Cut c = cut_of<D>(p.T, p.G);
+    if (fp32) qcache_write_kernel<D, float><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
+    else qcache_write_kernel<D, bf16><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t read_d(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
-    const int heads = heads_per_warp((p.T + 32 / (D / 16) - 1) / (32 / (D / 16)), p.G);
-    if (fp32) qcache_read_kernel<D, float><<<grid_of<D>(p.T, p.G, heads), 32 * kWarps, 0, stream>>>(p, heads);
-    else qcache_read_kernel<D, bf16><<<grid_of<D>(p.T, p.G, heads), 32 * kWarps, 0, stream>>>(p, heads);
+    const Cut c = cut_of<D>(p.T, p.G);
+    if (fp32) qcache_read_kernel<D, float><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
+    else qcache_read_kernel<D, bf16><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
     return cudaGetLastError();
 }
 

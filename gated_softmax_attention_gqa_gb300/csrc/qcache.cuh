@@ -53,25 +53,23 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {
     return r;
 }
 
-// Scale and centre of a group with extremes lo, hi (as bf16 bits and as the floats they
-// stand for) and the reciprocal that turns a distance from the centre into codes.  The
-// halves keep hi - lo finite over the whole fp32 range; a scale below the smallest
-// normal float stores the group as its centre.
+// Scale and centre of a group with extremes lo, hi (scale in the low half of `bits`) and
+// the reciprocal that turns a distance from the centre into codes.  The halves keep
+// hi - lo finite over the whole fp32 range; a scale below the smallest normal float stores
+// the group as its centre.  The reciprocal is one Newton step r (2 - s r) on the hardware
+// approximation, which for the 8-bit significands of bf16 is 1 / s rounded to nearest (the
+// tests compare every bf16 number).
 struct QcGroup {
-    uint32_t scale_bits, centre_bits;
+    uint32_t bits;
     float centre, inv;
 };
 __device__ __forceinline__ QcGroup qc_group(float lo, float hi) {
     const float step = __fmul_rn(__fsub_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo)), 2.0f / 15.0f);
-    const bool finite = step < INFINITY;  // false for NaN too
     QcGroup q;
-    const __nv_bfloat16 s = __float2bfloat16_rn(finite ? step : NAN);
-    const __nv_bfloat16 c = __float2bfloat16_rn(finite ? fmaf(8.0f, step, lo) : NAN);
-    q.scale_bits = __bfloat16_as_ushort(s);
-    q.centre_bits = __bfloat16_as_ushort(c);
-    q.centre = __bfloat162float(c);
-    const float sf = __bfloat162float(s);
-    q.inv = sf >= 1.17549435e-38f ? __frcp_rn(sf) : 0.f;
+    q.bits = step < INFINITY ? pack_bf16x2(step, fmaf(8.0f, step, lo)) : 0x7FC07FC0u;  // NaN, NaN
+    q.centre = bf16_hi(q.bits);
+    const float s = bf16_lo(q.bits), r = rcp_approx(s);
+    q.inv = s >= 1.17549435e-38f ? fmaf(r, fmaf(-s, r, 1.f), r) : 0.f;
     return q;
 }
 
@@ -102,16 +100,26 @@ __device__ __forceinline__ uint32_t qc_encode8(const float* x, const QcGroup& q)
 
 // sin and cos of the RoPE angle pos * f, f in 2^-64 turns: the product modulo one turn is
 // exact in integers, so the angle of a far position is as good as that of a near one
-// (a float product is off by half an ulp of the angle itself, 2e-3 rad at 32k).
+// (a float product is off by half an ulp of the angle itself, 2e-3 rad at 32k).  The rest
+// of the nearest quarter turn, at most pi/4, goes through the Taylor series of sine and
+// cosine (first terms left out: a^11/11! < 2e-9, a^12/12! < 2e-10).
 __device__ __forceinline__ void rope_turn_sincos(uint64_t f, int pos, float* s, float* c) {
     const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * f) >> 32);  // 2^-32 turns
     const uint32_t q = (t + 0x20000000u) >> 30;                         // nearest quarter turn
-    float s0, c0;
-    sincospif((float)(int32_t)(t - (q << 30)) * 4.656612873077393e-10f, &s0, &c0);  // 2^-31: half turns
-    const bool odd = q & 1u;
-    const float a = odd ? c0 : s0, b = odd ? s0 : c0;
-    *s = (q & 2u) ? -a : a;
-    *c = ((q + 1u) & 2u) ? -b : b;
+    const float a = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float a2 = a * a;
+    const float ps = fmaf(a2, fmaf(a2, fmaf(a2, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+    const float pc = fmaf(a2, fmaf(a2, fmaf(a2, fmaf(a2, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f);
+    const float s0 = fmaf(a * a2, ps, a), c0 = fmaf(a2, pc, 1.f);
+    const float x = q & 1u ? c0 : s0, y = q & 1u ? s0 : c0;
+    *s = __uint_as_float(__float_as_uint(x) ^ ((q & 2u) << 30));
+    *c = __uint_as_float(__float_as_uint(y) ^ (((q + 1u) & 2u) << 30));
+}
+
+// 1 / sqrt(x): the hardware approximation and one Newton step (0 for an infinite x).
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = rsqrtf(x);
+    return x < INFINITY ? fmaf(0.5f * r, fmaf(-x * r, r, 1.f), r) : r;
 }
 
 // Sequence of packed token t: the largest b with cu[b] <= t (B >= 1, cu[0] = 0).

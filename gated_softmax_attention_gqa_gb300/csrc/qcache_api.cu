@@ -34,6 +34,14 @@ void fill_turns(uint64_t* dst, int rd, double base) {
     std::memcpy(dst, last.turns, sizeof(uint64_t) * (rd / 2));
 }
 
+// floor(x / d) = floor(x m / 2^(31 + k)) for 0 <= x < 2^31, with 2^k the power of two at or
+// above d >= 2 and m = floor(2^(31 + k) / d) + 1 (m d exceeds 2^(31 + k) by at most d <= 2^k).
+PageDiv page_div(int d) {
+    int k = 0;
+    while (((int64_t)1 << k) < d) ++k;
+    return PageDiv{(uint32_t)((((uint64_t)1 << (31 + k)) / (uint64_t)d) + 1), (uint32_t)(k - 1)};
+}
+
 // The pool's geometry: what every entry point checks of it.
 gattn_status check_pool(const void* cache, const int32_t* table, int num_pages, int page_size, int max_pages, int B,
                         int G, int d) {
@@ -104,6 +112,7 @@ gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, cons
     p.num_pages = num_pages;
     p.page_size = page_size;
     p.max_pages = max_pages;
+    p.by_page = page_div(page_size);
     p.T = T;
     p.B = B;
     p.G = G;
@@ -139,6 +148,7 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
     p.num_pages = num_pages;
     p.page_size = page_size;
     p.max_pages = max_pages;
+    p.by_page = page_div(page_size);
     p.T = T;
     p.B = B;
     p.G = G;
