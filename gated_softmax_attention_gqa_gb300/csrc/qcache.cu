@@ -14,9 +14,16 @@
 namespace gattn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
-// Sixteen consecutive features of a row, as loaded.
+// Sixteen consecutive features, in pairs for the two-wide fp32 instructions: quad q's
+// features 4q, 4q + 2 in p[2q] and 4q + 1, 4q + 3 in p[2q + 1], so that a quad's codes
+// combine pair by pair too.
+struct Vec16 {
+    float2 p[8];
+};
+
+// A row's sixteen features as loaded.
 template <typename T>
 struct Row16;
 template <>
@@ -29,14 +36,14 @@ struct Row16<bf16> {
     }
     // features 8 c .. 8 c + 7 only, from p
     __device__ __forceinline__ void load8(int c, const bf16* p) { v[c] = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
+    __device__ __forceinline__ void get(Vec16& x) const {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[8 * c + 2 * i] = bf16_lo(w[i]);
-                x[8 * c + 2 * i + 1] = bf16_hi(w[i]);
+            for (int q = 0; q < 2; ++q) {
+                x.p[4 * c + 2 * q] = make_float2(bf16_lo(w[2 * q]), bf16_lo(w[2 * q + 1]));
+                x.p[4 * c + 2 * q + 1] = make_float2(bf16_hi(w[2 * q]), bf16_hi(w[2 * q + 1]));
             }
         }
     }
@@ -53,16 +60,39 @@ struct Row16<float> {
         v[2 * c] = reinterpret_cast<const float4*>(p)[0];
         v[2 * c + 1] = reinterpret_cast<const float4*>(p)[1];
     }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
+    __device__ __forceinline__ void get(Vec16& x) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[4 * i] = v[i].x;
-            x[4 * i + 1] = v[i].y;
-            x[4 * i + 2] = v[i].z;
-            x[4 * i + 3] = v[i].w;
+        for (int q = 0; q < 4; ++q) {
+            x.p[2 * q] = make_float2(v[q].x, v[q].z);
+            x.p[2 * q + 1] = make_float2(v[q].y, v[q].w);
         }
     }
 };
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The codes of eight features (four pairs), lowest feature in the lowest nibble.  CLAMP is
+// needed only where a group's own extremes fall outside [-8, 7] (codes are monotonic in x),
+// which takes a centre so large that its rounding is half a step.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t encode8(const float2* p, const QcGroup& g) {
+    uint32_t h[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float2 u[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u[i] = fma2(add2(p[2 * q + i], both(-g.centre)), both(g.inv), both(kQcMagic + 8.f));
+            if (CLAMP)
+                u[i] = make_float2(fminf(fmaxf(u[i].x, kQcMagic), kQcMagic + 15.f),
+                                   fminf(fmaxf(u[i].y, kQcMagic), kQcMagic + 15.f));
+        }
+        // magic + even code + 16 odd code: a byte in the low mantissa bits
+        const float2 b = fma2(add2(u[1], both(-kQcMagic)), both(16.f), u[0]);
+        h[q] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+    }
+    return __byte_perm(h[0], h[1], 0x5410);
+}
 
 // Place of packed token t: its position, and its row of the pool.  False for padding and
 // for tokens that a length or a table entry keeps out of the cache (the caller reports).
@@ -127,24 +157,24 @@ __device__ __forceinline__ bool report(int what, unsigned int* status) {
 
 // Quantise this lane's 16 features (two neighbouring lanes share a group of 32, four a
 // slab) and store them at row `row` of `block`.  All lanes of the warp.
-__device__ __forceinline__ void encode_store(const float (&x)[16], uint8_t* block, int row, int e0, int d, bool live) {
-    float hi = max_nan(x[0], x[1]), lo = min_nan(x[0], x[1]);
+__device__ __forceinline__ void encode_store(const Vec16& x, uint8_t* block, int row, int e0, int d, bool live) {
+    float hi = max_nan(x.p[0].x, x.p[0].y), lo = min_nan(x.p[0].x, x.p[0].y);
 #pragma unroll
-    for (int i = 2; i < 16; i += 2) {
-        hi = max_nan(hi, x[i], x[i + 1]);
-        lo = min_nan(lo, x[i], x[i + 1]);
+    for (int i = 1; i < 8; ++i) {
+        hi = max_nan(hi, x.p[i].x, x.p[i].y);
+        lo = min_nan(lo, x.p[i].x, x.p[i].y);
     }
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
     const QcGroup q = qc_group(lo, hi);
     uint32_t w[2];
-    const bool inside = qc_round(hi, q) <= kQcMagic + 7.f && qc_round(lo, q) >= kQcMagic - 8.f;
-    if (__all_sync(0xffffffffu, inside)) {
-        w[0] = qc_encode8<false>(x, q);
-        w[1] = qc_encode8<false>(x + 8, q);
+    const float2 ends = fma2(add2(make_float2(lo, hi), both(-q.centre)), both(q.inv), both(kQcMagic + 8.f));
+    if (__all_sync(0xffffffffu, ends.x >= kQcMagic && ends.y <= kQcMagic + 15.f)) {
+        w[0] = encode8<false>(x.p, q);
+        w[1] = encode8<false>(x.p + 4, q);
     } else {
-        w[0] = qc_encode8<true>(x, q);
-        w[1] = qc_encode8<true>(x + 8, q);
+        w[0] = encode8<true>(x.p, q);
+        w[1] = encode8<true>(x.p + 4, q);
     }
     // lanes j and j + 2 of a slab hold features 16 j .. and 32 + 16 j ..: together the words
     // 4 j .. 4 j + 3, of which lane j stores the first two and lane j + 2 the others
@@ -162,7 +192,7 @@ __device__ __forceinline__ void encode_store(const float (&x)[16], uint8_t* bloc
 // A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass of a warp; a warp
 // takes `passes` of them and walks heads [blockIdx.y heads, ...) in each.
 template <int D, typename T>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     __shared__ __align__(16) float2 tables[kWarps][TPW * D / 2 + 8];
@@ -202,17 +232,6 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     const bool ok = report(lane < passes * TPW ? place_new(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
 
-    float w[16], m[16];  // norm weights, and the partners' with the rotation's sign
-    {
-        Row16<T> wr;
-        wr.load(static_cast<const T*>(p.knorm_w) + e0);
-        wr.get(w);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) wr.load8(c, static_cast<const T*>(p.knorm_w) + e0 + 8 * c + mate[c]);
-        wr.get(m);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m[i] = mate[i >> 3] > 0 ? -m[i] : m[i];
-    }
     float2* table = tables[warp];
     const float2* sc[2];
 #pragma unroll
@@ -234,14 +253,24 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         }
         __syncwarp();
         // K' = (x wc + partner ws) / rms
-        float wc[16], ws[16];
+        Vec16 wc, ws;
+        {
+            Row16<T> wr;
+            wr.load(static_cast<const T*>(p.knorm_w) + e0);
+            wr.get(wc);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float4 v = *reinterpret_cast<const float4*>(sc[i >> 3] + (i & 7));
-            wc[i] = w[i] * v.y;
-            ws[i] = m[i] * v.x;
-            wc[i + 1] = w[i + 1] * v.w;
-            ws[i + 1] = m[i + 1] * v.z;
+            for (int c = 0; c < 2; ++c) wr.load8(c, static_cast<const T*>(p.knorm_w) + e0 + 8 * c + mate[c]);
+            wr.get(ws);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // the partner of a first half's feature enters with -sin
+                const float4 a = *reinterpret_cast<const float4*>(sc[q >> 1] + 4 * (q & 1));
+                const float4 b = *reinterpret_cast<const float4*>(sc[q >> 1] + 4 * (q & 1) + 2);
+                const float2 sign = both(mate[q >> 1] > 0 ? -1.f : 1.f);
+                wc.p[2 * q] = mul2(wc.p[2 * q], make_float2(a.y, b.y));
+                wc.p[2 * q + 1] = mul2(wc.p[2 * q + 1], make_float2(a.w, b.w));
+                ws.p[2 * q] = mul2(ws.p[2 * q], mul2(make_float2(a.x, b.x), sign));
+                ws.p[2 * q + 1] = mul2(ws.p[2 * q + 1], mul2(make_float2(a.z, b.z), sign));
+            }
         }
         const Place at = place_of(mine, pass * TPW + lane / LPR);
         const bool live = at.page >= 0;
@@ -250,7 +279,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         for (int g = 0; g < n_heads; ++g) {
             vr.load(vp);
             vp += p.v_head_stride;
-            float x[16], o[16], ss = 0.f;
+            Vec16 x, o;
             kr.get(x);
             ko.get(o);
             // the next K rows: the next head's, or the next pass's first
@@ -261,13 +290,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                 start(pass + 1);
                 load_k();
             }
+            float2 s2 = mul2(x.p[0], x.p[0]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 1; i < 8; ++i) s2 = fma2(x.p[i], x.p[i], s2);
+            float ss = s2.x + s2.y;
 #pragma unroll
             for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-            const float rinv = inv_sqrt(ss / (float)D + p.eps);
+            const float2 rinv = both(inv_sqrt(ss / (float)D + p.eps));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fmaf(x[i], wc[i], o[i] * ws[i]) * rinv;
+            for (int i = 0; i < 8; ++i) x.p[i] = mul2(fma2(x.p[i], wc.p[i], mul2(o.p[i], ws.p[i])), rinv);
             encode_store(x, block, row, e0, D, live);
             vr.get(x);
             encode_store(x, block + plane, row, e0, D, live);
@@ -326,7 +357,7 @@ __global__ void __launch_bounds__(32 * kWarps)
         const int par = 8 * D + ((e0 >> 5) * 16 + row) * 2 - ((e0 >> 6) * 512 + row * 32 + 16 * j);
         T* kout = static_cast<T*>(p.k) + (t * p.G + g0) * D + e0;
         T* vout = static_cast<T*>(p.v) + (t * p.G + g0) * D + e0;
-#pragma unroll 2
+#pragma unroll 4
         for (int g = 0; g < n_heads; ++g) {
             uint4 w[2];
             uint32_t s[2], c[2];
@@ -360,7 +391,7 @@ template <int D>
 Cut cut_of(int T, int G) {
     constexpr int TPW = 32 / (D / 16);
     const int64_t want = 16 * (int64_t)device_sm_count();
-    Cut c{4, G, dim3()};
+    Cut c{2, G, dim3()};
     auto warps = [&]() { return ((int64_t)T + TPW * c.passes - 1) / (TPW * c.passes) * ((G + c.heads - 1) / c.heads); };
     while (c.passes > 1 && warps() < want) c.passes /= 2;
     while (c.heads > 1 && warps() < want) c.heads = (c.heads + 1) / 2;

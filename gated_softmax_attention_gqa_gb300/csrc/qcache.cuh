@@ -73,30 +73,9 @@ __device__ __forceinline__ QcGroup qc_group(float lo, float hi) {
     return q;
 }
 
-// Eight codes of one group as nibbles, lowest feature first.  Adding 1.5 * 2^23 rounds
-// the product to an integer half to even in one rounding and leaves code - 8 in the low
-// mantissa bits (two's complement); flipping bit 3 of each nibble adds the 8.  CLAMP is
-// needed only where a group's own extremes fall outside [-8, 7] (the codes are monotonic
-// in x), which takes a centre so large that its rounding is half a step.
+// Adding 1.5 * 2^23 + 8 to (x - centre) / scale rounds it to an integer half to even, in the
+// one rounding of a fused multiply-add, and leaves the code in the low mantissa bits.
 constexpr float kQcMagic = 12582912.f;
-__device__ __forceinline__ float qc_round(float x, const QcGroup& q) {
-    return fmaf(__fsub_rn(x, q.centre), q.inv, kQcMagic);
-}
-template <bool CLAMP>
-__device__ __forceinline__ uint32_t qc_encode8(const float* x, const QcGroup& q) {
-    uint32_t b[4];  // byte i: features 2i (low nibble) and 2i + 1; garbage above it
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float t0 = qc_round(x[2 * i], q), t1 = qc_round(x[2 * i + 1], q);
-        if (CLAMP) {
-            t0 = fminf(fmaxf(t0, kQcMagic - 8.f), kQcMagic + 7.f);
-            t1 = fminf(fmaxf(t1, kQcMagic - 8.f), kQcMagic + 7.f);
-        }
-        const uint32_t hi = __float_as_uint(t1) << 4;
-        b[i] = (__float_as_uint(t0) & 15u) | (hi & ~15u);
-    }
-    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^ 0x88888888u;
-}
 
 // sin and cos of the RoPE angle pos * f, f in 2^-64 turns: the product modulo one turn is
 // exact in integers, so the angle of a far position is as good as that of a near one
