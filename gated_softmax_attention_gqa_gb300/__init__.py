@@ -355,42 +355,57 @@ def gattn_qcache_shape(num_pages, G, page_size, d):
     return (2, num_pages, G, page_size // 16, 10 * d)
 
 
-def _qcache_geometry(qcache, block_table, B):
-    """(num_pages, G, page_size, d, max_pages) of a cache and its table, checked."""
-    if qcache.dim() != 5 or qcache.shape[0] != 2 or qcache.dtype != torch.uint8 or not qcache.is_contiguous():
+# A decode step is a few microseconds on the GPU, so these wrappers stay lean: device
+# indices instead of device objects, the raw handle of the current stream, no helper
+# objects per call.
+
+def _qcache_geometry(qcache, block_table):
+    """(num_pages, G, page_size, d, B, max_pages, device index) of a cache and its table, checked."""
+    if qcache.dim() != 5 or block_table.dim() != 2:
+        raise ValueError("qcache is [2,num_pages,G,page_size/16,10 d], block_table [B,max_pages]")
+    planes, num_pages, G, blocks, row = qcache.shape
+    if planes != 2 or row % 10 or qcache.dtype is not torch.uint8 or not qcache.is_contiguous():
         raise ValueError("qcache must be a contiguous uint8 [2,num_pages,G,page_size/16,10 d] tensor")
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 [B,max_pages] tensor")
-    if block_table.shape[0] != B or block_table.device != qcache.device:
-        raise ValueError(f"block_table must have one row for each of {B} sequences, on the cache's device")
-    _, num_pages, G, blocks, row = qcache.shape
-    if row % 10:
-        raise ValueError("qcache: the last dimension is 10 d bytes")
-    return num_pages, G, 16 * blocks, row // 10, block_table.shape[1]
+    dev = qcache.get_device()
+    if block_table.dtype is not torch.int32 or not block_table.is_contiguous() or block_table.get_device() != dev:
+        raise ValueError("block_table must be a contiguous int32 [B,max_pages] tensor on the cache's device")
+    B, max_pages = block_table.shape
+    return num_pages, G, 16 * blocks, row // 10, B, max_pages, dev
 
 
-def _qcache_index(name, t, n, device):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+def _qcache_index(name, t, n, dev):
+    if t.shape != (n,) or t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous int32 tensor of {n} on the cache's device")
     return t.data_ptr()
 
 
-def _qcache_stride(t, i, name):
-    """Stride of dimension i for the C call, where 0 selects the contiguous default: a
-    dimension of one has no stride to speak of, and a broadcast one cannot be passed."""
-    if t.shape[i] <= 1:
-        return 0
-    if t.stride(i) == 0:
-        raise ValueError(f"{name}: broadcast (stride 0) views are not supported; pass a contiguous copy")
-    return t.stride(i)
+def _qcache_dense(name, t, shape, dtype, dev):
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the cache's device")
+    return t.data_ptr()
 
 
-def _qcache_call(device, stream, fn, *args):
-    """fn(*args, stream handle) with the tensors' device current."""
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
+def _qcache_strides(t, n, name):
+    """Strides of the first n dimensions for the C call, where 0 selects the contiguous
+    default: a dimension of one has no stride to speak of, and a broadcast one cannot be passed."""
+    out = []
+    for size, stride in zip(t.shape[:n], t.stride()):
+        if size <= 1:
+            stride = 0
+        elif stride == 0:
+            raise ValueError(f"{name}: broadcast (stride 0) views are not supported; pass a contiguous copy")
+        out.append(stride)
+    return out
+
+
+def _qcache_call(dev, stream, fn, *args):
+    """fn(*args, stream handle) with device `dev` current."""
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
         return fn(*args, s)
-    with torch.cuda.device(device):
+    with torch.cuda.device(dev):
         return fn(*args, s)
 
 
@@ -409,30 +424,27 @@ def gattn_qcache_write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens=N
     k, v [T,G,d] raw projections, bf16 or fp32, the last dimension contiguous (views into
     a fused projection are fine); knorm_w [d] of the same dtype; K is normed and rotated.
     cu_seqlens [B+1] int32 on the device: sequence b's new tokens are rows cu_seqlens[b] ..
-    cu_seqlens[b+1]-1 (rows past the last are ignored); None: one token per sequence.
+    cu_seqlens[b+1]-1 (rows past the last are ignored); None: one token per sequence, and a
+    length of 0 marks an unused row.
     seqlens [B] int32 on the device: tokens in each sequence after the write.
     block_table [B,max_pages] int32: the page of each page_size-token stretch."""
-    if k.dim() != 3 or v.shape != k.shape or k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("k and v must be [T,G,d] with a contiguous last dimension")
-    if k.dtype not in DTYPES or v.dtype != k.dtype or knorm_w.dtype != k.dtype:
-        raise ValueError("k, v and knorm_w must all be bfloat16 or all be float32")
-    T, G, d = k.shape
-    B = seqlens.shape[0]
-    num_pages, cG, page_size, cd, max_pages = _qcache_geometry(qcache, block_table, B)
-    device = qcache.device
-    if (cG, cd) != (G, d) or knorm_w.shape != (d,) or not knorm_w.is_contiguous():
-        raise ValueError(f"the cache holds {cG} heads of {cd}, k and v {G} of {d}; knorm_w must be a contiguous [{d}]")
-    if k.device != device or v.device != device or knorm_w.device != device:
-        raise ValueError("k, v, knorm_w and the cache must be on one device")
+    num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
+    dtype = k.dtype
+    if k.dim() != 3 or v.shape != k.shape or k.stride(2) != 1 or v.stride(2) != 1 or k.shape[1:] != (G, d):
+        raise ValueError(f"k and v must be [T,{G},{d}] as the cache's heads, with a contiguous last dimension")
+    if dtype not in DTYPES or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("k and v must both be bfloat16 or both be float32, on the cache's device")
+    T = k.shape[0]
     if cu_seqlens is None and T != B:
         raise ValueError(f"without cu_seqlens every sequence gets one token: {T} tokens, {B} sequences")
-    ks, kh, vs, vh = (_qcache_stride(t, i, "k, v") for t in (k, v) for i in (0, 1))
     st = _qcache_call(
-        device, stream, _lib.load().gattn_qcache_write, k.data_ptr(), v.data_ptr(), qcache.data_ptr(),
-        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, device),
-        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, device), knorm_w.data_ptr(),
-        T, B, G, d, rotary_dim, rope_base, eps, ks, kh, vs, vh, DTYPES[k.dtype])
-    check(st, "gattn_qcache_write")
+        dev, stream, _lib.load().gattn_qcache_write, k.data_ptr(), v.data_ptr(), qcache.data_ptr(),
+        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, dev),
+        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, dev),
+        _qcache_dense("knorm_w", knorm_w, (d,), dtype, dev), T, B, G, d, rotary_dim, rope_base, eps,
+        *_qcache_strides(k, 2, "k"), *_qcache_strides(v, 2, "v"), DTYPES[dtype])
+    if st:
+        check(st, "gattn_qcache_write")
     return qcache
 
 
@@ -445,34 +457,33 @@ def gattn_qcache_read(qcache, block_table, starts=None, cu_seqlens=None, *, tota
     sequence b; both are int32 on the device.  cu_seqlens None: one token per sequence
     (total = B); starts None: from token 0.  total is the number of rows, cu_seqlens[B] or
     more (rows past it are left as they were).  k_out, v_out: contiguous tensors to fill."""
-    B = block_table.shape[0]
-    num_pages, G, page_size, d, max_pages = _qcache_geometry(qcache, block_table, B)
-    device = qcache.device
+    num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
     if total is None:
-        total = B if cu_seqlens is None else None if k_out is None else k_out.shape[0]
-    if total is None:
-        raise ValueError("total (the number of rows) is needed with cu_seqlens")
+        if cu_seqlens is not None and k_out is None:
+            raise ValueError("total (the number of rows) is needed with cu_seqlens")
+        total = B if cu_seqlens is None else k_out.shape[0]
     if cu_seqlens is None and total != B:
         raise ValueError("without cu_seqlens one token of each sequence is read")
-    if (k_out is None) != (v_out is None):
+    if k_out is not None and v_out is not None:
+        dtype = k_out.dtype
+    elif k_out is not None or v_out is not None:
         raise ValueError("k_out and v_out go together")
+    if dtype not in DTYPES:
+        raise ValueError("the values are returned in bfloat16 or float32")
     if k_out is None:
-        if dtype not in DTYPES:
-            raise ValueError("dtype must be bfloat16 or float32")
-        k_out = _empty_on(stream, (total, G, d), dtype, device)
-        v_out = _empty_on(stream, (total, G, d), dtype, device)
+        k_out = _empty_on(stream, (total, G, d), dtype, qcache.device)
+        v_out = _empty_on(stream, (total, G, d), dtype, qcache.device)
+        kp, vp = k_out.data_ptr(), v_out.data_ptr()
     else:
-        for t in (k_out, v_out):
-            if t.shape != (total, G, d) or t.dtype not in DTYPES or not t.is_contiguous() or t.device != device:
-                raise ValueError(f"k_out and v_out must be contiguous bf16 or fp32 [{total},{G},{d}] tensors")
-        if k_out.dtype != v_out.dtype:
-            raise ValueError("k_out and v_out must have one dtype")
+        kp = _qcache_dense("k_out", k_out, (total, G, d), dtype, dev)
+        vp = _qcache_dense("v_out", v_out, (total, G, d), dtype, dev)
     st = _qcache_call(
-        device, stream, _lib.load().gattn_qcache_read, qcache.data_ptr(), block_table.data_ptr(), num_pages, page_size,
-        max_pages, None if starts is None else _qcache_index("starts", starts, B, device),
-        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, device), total, B, G, d,
-        DTYPES[k_out.dtype], k_out.data_ptr(), v_out.data_ptr())
-    check(st, "gattn_qcache_read")
+        dev, stream, _lib.load().gattn_qcache_read, qcache.data_ptr(), block_table.data_ptr(), num_pages, page_size,
+        max_pages, None if starts is None else _qcache_index("starts", starts, B, dev),
+        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, dev), total, B, G, d,
+        DTYPES[dtype], kp, vp)
+    if st:
+        check(st, "gattn_qcache_read")
     return k_out, v_out
 
 
@@ -490,48 +501,45 @@ def gattn_decode_qcache(q_new, qcache, block_table, seqlens, gate, qnorm_w, *, r
     [B,G,d] and knorm_w the new token is first written into the cache.  The rest as
     gattn_decode_paged.  Returns out [B,H*d]."""
     mode = _mode(gate_mode, gate_act, gate_additive)
-    if q_new.dim() != 3 or q_new.stride(2) != 1 or q_new.dtype != torch.bfloat16:
-        raise ValueError("q_new must be a bfloat16 [B,H,d] tensor with a contiguous last dimension")
-    B, H, d = q_new.shape
-    num_pages, G, page_size, cd, max_pages = _qcache_geometry(qcache, block_table, B)
-    device = qcache.device
-    if cd != d or qnorm_w.shape != (d,) or qnorm_w.dtype != torch.bfloat16 or not qnorm_w.is_contiguous():
-        raise ValueError(f"head_dim: q_new {d}, cache {cd}; qnorm_w must be a contiguous bfloat16 [{d}]")
-    if q_new.device != device or qnorm_w.device != device:
-        raise ValueError("q_new, qnorm_w and the cache must be on one device")
+    num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
+    if q_new.dim() != 3 or q_new.dtype is not torch.bfloat16 or q_new.stride(2) != 1 or q_new.get_device() != dev:
+        raise ValueError("q_new must be a bfloat16 [B,H,d] tensor with a contiguous last dimension, on the cache's device")
+    H = q_new.shape[1]
+    if q_new.shape != (B, H, d):
+        raise ValueError(f"q_new is {list(q_new.shape)}: the table has {B} sequences and the cache heads of {d}")
     layout = mode & 0x0F
     gp, gs, gh = None, 0, 0
     if layout:
         want = (B, H, d) if layout == 1 else (B, H) if layout == 2 else (B, d)
-        if gate is None or gate.shape != want or gate.dtype != torch.bfloat16 or gate.device != device:
+        if gate is None or gate.shape != want or gate.dtype is not torch.bfloat16 or gate.get_device() != dev:
             raise ValueError(f"gate must be a bfloat16 {list(want)} tensor on the cache's device")
         if layout != 2 and gate.stride(-1) != 1:
             raise ValueError("gate: the last dimension must be contiguous")
-        gp, gs = gate.data_ptr(), _qcache_stride(gate, 0, "gate")
-        gh = _qcache_stride(gate, 1, "gate") if layout != 3 else 0
+        gp = gate.data_ptr()
+        gs, gh = _qcache_strides(gate, 2, "gate") if layout != 3 else (*_qcache_strides(gate, 1, "gate"), 0)
     kp = vp = wp = None
     if k_new is not None or v_new is not None or knorm_w is not None:
         if k_new is None or v_new is None or knorm_w is None:
             raise ValueError("an append needs k_new, v_new and knorm_w")
-        for name, t, shape in (("k_new", k_new, (B, G, d)), ("v_new", v_new, (B, G, d)), ("knorm_w", knorm_w, (d,))):
-            if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
-                raise ValueError(f"{name} must be a contiguous bfloat16 {list(shape)} tensor on the cache's device")
-        kp, vp, wp = k_new.data_ptr(), v_new.data_ptr(), knorm_w.data_ptr()
+        kp = _qcache_dense("k_new", k_new, (B, G, d), torch.bfloat16, dev)
+        vp = _qcache_dense("v_new", v_new, (B, G, d), torch.bfloat16, dev)
+        wp = _qcache_dense("knorm_w", knorm_w, (d,), torch.bfloat16, dev)
     if out is None:
-        out = _empty_on(stream, (B, H * d), torch.bfloat16, device)
-    elif out.shape != (B, H * d) or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != device:
-        raise ValueError(f"out must be a contiguous bfloat16 [{B},{H * d}] tensor on the cache's device")
+        out = _empty_on(stream, (B, H * d), torch.bfloat16, qcache.device)
+        op = out.data_ptr()
+    else:
+        op = _qcache_dense("out", out, (B, H * d), torch.bfloat16, dev)
     if workspace is None:
-        with torch.cuda.device(device):
+        with torch.cuda.device(qcache.device):
             need = gattn_decode_qcache_workspace_size(B, H, G, d, max_pages * page_size)
-        workspace = _empty_on(stream, (max(need, 1),), torch.uint8, device)
-    elif not workspace.is_contiguous() or workspace.device != device:
+        workspace = _empty_on(stream, (max(need, 1),), torch.uint8, qcache.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     st = _qcache_call(
-        device, stream, _lib.load().gattn_decode_qcache, q_new.data_ptr(), kp, vp, qcache.data_ptr(),
-        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, device), gp,
-        qnorm_w.data_ptr(), wp, B, H, G, d, rotary_dim, rope_base, eps, mode, _qcache_stride(q_new, 0, "q_new"),
-        _qcache_stride(q_new, 1, "q_new"), gs, gh, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        out.data_ptr())
-    check(st, "gattn_decode_qcache")
+        dev, stream, _lib.load().gattn_decode_qcache, q_new.data_ptr(), kp, vp, qcache.data_ptr(),
+        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, dev), gp,
+        _qcache_dense("qnorm_w", qnorm_w, (d,), torch.bfloat16, dev), wp, B, H, G, d, rotary_dim, rope_base, eps, mode,
+        *_qcache_strides(q_new, 2, "q_new"), gs, gh, workspace.data_ptr(), workspace.nbytes, op)
+    if st:
+        check(st, "gattn_decode_qcache")
     return out
