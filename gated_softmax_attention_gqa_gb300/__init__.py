@@ -385,17 +385,14 @@ def _qcache_dense(name, t, shape, dtype, dev):
     return t.data_ptr()
 
 
-def _qcache_strides(t, n, name):
-    """Strides of the first n dimensions for the C call, where 0 selects the contiguous
-    default: a dimension of one has no stride to speak of, and a broadcast one cannot be passed."""
-    out = []
-    for size, stride in zip(t.shape[:n], t.stride()):
-        if size <= 1:
-            stride = 0
-        elif stride == 0:
-            raise ValueError(f"{name}: broadcast (stride 0) views are not supported; pass a contiguous copy")
-        out.append(stride)
-    return out
+def _qcache_stride(size, stride, name):
+    """A dimension's stride for the C call, where 0 selects the contiguous default: a
+    dimension of one has no stride to speak of, and a broadcast one cannot be passed."""
+    if size <= 1:
+        return 0
+    if stride == 0:
+        raise ValueError(f"{name}: broadcast (stride 0) views are not supported; pass a contiguous copy")
+    return stride
 
 
 def _qcache_call(dev, stream, fn, *args):
@@ -430,11 +427,14 @@ def gattn_qcache_write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens=N
     block_table [B,max_pages] int32: the page of each page_size-token stretch."""
     num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
     dtype = k.dtype
-    if k.dim() != 3 or v.shape != k.shape or k.stride(2) != 1 or v.stride(2) != 1 or k.shape[1:] != (G, d):
-        raise ValueError(f"k and v must be [T,{G},{d}] as the cache's heads, with a contiguous last dimension")
+    if k.dim() != 3 or k.shape != v.shape or k.shape != (k.shape[0], G, d):
+        raise ValueError(f"k and v must both be [T,{G},{d}], as the cache's heads")
+    T = k.shape[0]
+    (kt, kh, ke), (vt, vh, ve) = k.stride(), v.stride()
+    if ke != 1 or ve != 1:
+        raise ValueError("k and v: the last dimension must be contiguous")
     if dtype not in DTYPES or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v must both be bfloat16 or both be float32, on the cache's device")
-    T = k.shape[0]
     if cu_seqlens is None and T != B:
         raise ValueError(f"without cu_seqlens every sequence gets one token: {T} tokens, {B} sequences")
     st = _qcache_call(
@@ -442,7 +442,8 @@ def gattn_qcache_write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens=N
         block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, dev),
         None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, dev),
         _qcache_dense("knorm_w", knorm_w, (d,), dtype, dev), T, B, G, d, rotary_dim, rope_base, eps,
-        *_qcache_strides(k, 2, "k"), *_qcache_strides(v, 2, "v"), DTYPES[dtype])
+        _qcache_stride(T, kt, "k"), _qcache_stride(G, kh, "k"), _qcache_stride(T, vt, "v"), _qcache_stride(G, vh, "v"),
+        DTYPES[dtype])
     if st:
         check(st, "gattn_qcache_write")
     return qcache
@@ -502,11 +503,12 @@ def gattn_decode_qcache(q_new, qcache, block_table, seqlens, gate, qnorm_w, *, r
     gattn_decode_paged.  Returns out [B,H*d]."""
     mode = _mode(gate_mode, gate_act, gate_additive)
     num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
-    if q_new.dim() != 3 or q_new.dtype is not torch.bfloat16 or q_new.stride(2) != 1 or q_new.get_device() != dev:
-        raise ValueError("q_new must be a bfloat16 [B,H,d] tensor with a contiguous last dimension, on the cache's device")
-    H = q_new.shape[1]
-    if q_new.shape != (B, H, d):
-        raise ValueError(f"q_new is {list(q_new.shape)}: the table has {B} sequences and the cache heads of {d}")
+    if q_new.dim() != 3 or q_new.dtype is not torch.bfloat16 or q_new.get_device() != dev:
+        raise ValueError("q_new must be a bfloat16 [B,H,d] tensor on the cache's device")
+    qb, H, qd = q_new.shape
+    qs, qh, qe = q_new.stride()
+    if qb != B or qd != d or qe != 1:
+        raise ValueError(f"q_new must be [{B},H,{d}], as the table and the cache, its last dimension contiguous")
     layout = mode & 0x0F
     gp, gs, gh = None, 0, 0
     if layout:
@@ -515,8 +517,9 @@ def gattn_decode_qcache(q_new, qcache, block_table, seqlens, gate, qnorm_w, *, r
             raise ValueError(f"gate must be a bfloat16 {list(want)} tensor on the cache's device")
         if layout != 2 and gate.stride(-1) != 1:
             raise ValueError("gate: the last dimension must be contiguous")
-        gp = gate.data_ptr()
-        gs, gh = _qcache_strides(gate, 2, "gate") if layout != 3 else (*_qcache_strides(gate, 1, "gate"), 0)
+        gp, gs = gate.data_ptr(), _qcache_stride(B, gate.stride(0), "gate")
+        if layout != 3:
+            gh = _qcache_stride(H, gate.stride(1), "gate")
     kp = vp = wp = None
     if k_new is not None or v_new is not None or knorm_w is not None:
         if k_new is None or v_new is None or knorm_w is None:
@@ -539,7 +542,7 @@ def gattn_decode_qcache(q_new, qcache, block_table, seqlens, gate, qnorm_w, *, r
         dev, stream, _lib.load().gattn_decode_qcache, q_new.data_ptr(), kp, vp, qcache.data_ptr(),
         block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, dev), gp,
         _qcache_dense("qnorm_w", qnorm_w, (d,), torch.bfloat16, dev), wp, B, H, G, d, rotary_dim, rope_base, eps, mode,
-        *_qcache_strides(q_new, 2, "q_new"), gs, gh, workspace.data_ptr(), workspace.nbytes, op)
+        _qcache_stride(B, qs, "q_new"), _qcache_stride(H, qh, "q_new"), gs, gh, workspace.data_ptr(), workspace.nbytes, op)
     if st:
         check(st, "gattn_decode_qcache")
     return out
