@@ -47,14 +47,11 @@ constexpr int kPieceTiles = 2;
 template <int D>
 struct QdCfg {
     static constexpr int NG = D / kQcGroup;             // scale groups
-    // 16-token blocks a warp takes of a tile.  Two share the copies, waits and softmax
-    // bookkeeping (some 250 instructions a step next to 230 a block at d = 128) and give the
-    // scheduler independent work; at d = 256 a deeper ring is worth more than that.
-    static constexpr int NB = D == 256 ? 1 : 2;
+    static constexpr int NB = 2;
     static constexpr int BT = NW * NB * kQcBlock;       // keys per tile
     static constexpr int BLOCK_BYTES = 10 * D;          // one 16-token block
     static constexpr int STAGE_BYTES = 2 * NB * BLOCK_BYTES;  // a warp's K and V blocks
-    static constexpr int CTAS_PER_SM = D == 256 ? 3 : 4;
+    static constexpr int CTAS_PER_SM = D == 256 ? 2 : 4;
     static constexpr int MAX_STAGES = 8;                // per warp
     static constexpr int OROW = D + 4;                  // floats per row of the merge buffer (banks)
     // shared memory: the warps' rings (NW * stages), then
@@ -66,8 +63,21 @@ struct QdCfg {
     static constexpr int OFF_TOT = OFF_ML + NW * 64;         // float [8][2] the merged (max, sum)
     static constexpr int OFF_BAR = OFF_TOT + 64;             // mbarrier [NW][MAX_STAGES]
     static constexpr int OFF_MISC = OFF_BAR + NW * 8 * MAX_STAGES;
-    static constexpr int OFF_RED = OFF_MISC + 16;            // int [NW] scan scratch
-    static constexpr int OFF_OBUF = OFF_RED + 16;            // float [r][OROW]; the sine table (rd/2 float2) before it
+    static constexpr int OFF_RED = OFF_MISC + 16;            // int [NW][2] scan scratch
+    static constexpr int OFF_OBUF = OFF_RED + 32;            // float [r][OROW]; the sine table (rd/2 float2) before it
+};
+
+// What a CTA keeps of the batch in shared memory.
+struct Sequences {
+    int* tiles;     // [B + 1] tiles of the sequences ahead of each (one KV head)
+    int* lens;      // [B]
+    uint16_t* live; // [B + 1] sequences with any tile ahead of each
+    __host__ __device__ static int bytes(int B) { return 4 * (B + 1) + 4 * B + 2 * (B + 2); }
+    __device__ Sequences(uint8_t* at, int B) {
+        tiles = reinterpret_cast<int*>(at);
+        lens = tiles + B + 1;
+        live = reinterpret_cast<uint16_t*>(lens + B);
+    }
 };
 
 // Bytes of the merge buffer / sine table, and of everything behind the rings.
@@ -78,7 +88,7 @@ __host__ __device__ int obuf_bytes(int r, int rd) {
 }
 template <int D>
 __host__ __device__ int tail_bytes(int B, int r, int rd) {
-    return QdCfg<D>::OFF_OBUF + obuf_bytes<D>(r, rd) + 4 * (2 * B + 1);
+    return QdCfg<D>::OFF_OBUF + obuf_bytes<D>(r, rd) + Sequences::bytes(B);
 }
 
 template <int D>
@@ -86,67 +96,98 @@ __device__ __forceinline__ int seq_tiles(int L, int Lmax) {
     return (L >= 1 && L <= Lmax) ? (L + QdCfg<D>::BT - 1) / QdCfg<D>::BT : 0;
 }
 
-// Work units of one KV head of a sequence: its tiles and, ahead of them, kPieceTiles that
-// stand for the piece itself.
-template <int D>
-__device__ __forceinline__ int seq_units(int L, int Lmax) {
-    const int n = seq_tiles<D>(L, Lmax);
-    return n ? n + kPieceTiles : 0;
-}
+// The work split counts units: a (sequence, KV head) piece is kPieceTiles units that stand
+// for starting and merging it, then one unit a tile.  CTA c of N takes the units from
+// start(c) on; there are no more CTAs than units, so none between two that hold parts of a
+// sequence is empty.  (The host refuses batches of 2^31 units.)
+struct WorkSplit {
+    int N, base, rem;
+    __device__ WorkSplit(int units, int n_ctas) {
+        N = units < n_ctas ? units : n_ctas;
+        base = N ? units / N : 0;
+        rem = units - base * N;
+    }
+    __device__ int start(int c) const { return c * base + min(c, rem); }
+    __device__ int owner(int u) const {  // the CTA that holds unit u
+        const int wide = rem * (base + 1);
+        return u < wide ? u / (base + 1) : rem + (u - wide) / base;
+    }
+};
 
-// Exclusive prefix of the sequences' units into pb[0..B], and their lengths; all threads.
+// Fills `q` for the whole batch; all threads.
 template <int D>
-__device__ void unit_prefix(const int32_t* seqlens, int B, int Lmax, int* pb, int* lens, int* red) {
+__device__ void scan_batch(const int32_t* seqlens, int B, int Lmax, const Sequences& q, int* red) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int carry = 0;
-    for (int base = 0; base < B; base += THREADS) {
-        const int i = base + tid;
-        const int L = i < B ? seqlens[i] : 0;
-        int v = seq_units<D>(L, Lmax);
-        if (i < B) lens[i] = L;
+    int tiles0 = 0, live0 = 0;
+    for (int first = 0; first < B; first += THREADS) {
+        const int i = first + tid, L = i < B ? seqlens[i] : 0;
+        int v = seq_tiles<D>(L, Lmax);
+        const uint32_t any = __ballot_sync(0xffffffffu, v > 0);
+        const int n = __popc(any & ((2u << lane) - 1u));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += n;
+            const int up = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += up;
         }
-        if (lane == 31) red[warp] = v;
+        if (lane == 31) {
+            red[2 * warp] = v;
+            red[2 * warp + 1] = n;
+        }
         __syncthreads();
-        int before = carry, total = 0;
+        int t = tiles0, l = live0;
+#pragma unroll
         for (int w = 0; w < NW; ++w) {
-            if (w < warp) before += red[w];
-            total += red[w];
+            if (w == warp && i < B) {
+                q.tiles[i + 1] = t + v;
+                q.live[i + 1] = (uint16_t)(l + n);
+                q.lens[i] = L;
+            }
+            t += red[2 * w];
+            l += red[2 * w + 1];
         }
-        if (i < B) pb[i + 1] = before + v;
+        tiles0 = t;
+        live0 = l;
         __syncthreads();
-        carry += total;
     }
-    if (tid == 0) pb[0] = 0;
+    if (tid == 0) q.tiles[0] = q.live[0] = 0;
     __syncthreads();
 }
 
-// CTAs that share U units: no more than there are, so none between two that hold parts of
-// a sequence is empty.
-__device__ __forceinline__ int active_ctas(int64_t U, int n_ctas) { return U < n_ctas ? (int)U : n_ctas; }
+// How many tiles lie ahead of unit u.
+__device__ __forceinline__ int tiles_ahead(int u, const Sequences& q, int B, int G) {
+    int lo = 0, hi = B - 1;  // largest b with G * units(b) <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (G * (q.tiles[mid] + kPieceTiles * q.live[mid]) <= u) lo = mid; else hi = mid - 1;
+    }
+    const int nt = q.tiles[lo + 1] - q.tiles[lo];
+    const int rel = u - G * (q.tiles[lo] + kPieceTiles * q.live[lo]);
+    if (nt == 0) return G * q.tiles[lo];  // past the last piece
+    const int g = (int)((unsigned)rel / (unsigned)(nt + kPieceTiles)), i = rel - g * (nt + kPieceTiles) - kPieceTiles;
+    return G * q.tiles[lo] + g * nt + max(i, 0);
+}
 
-// Unit u of the global list: sequence b, KV head g, tile i of nt (negative: the piece's own units).
+// Tile x of the batch: sequence b, KV head g, tile i of its nt.
 struct TileAt {
     int b, g, i, nt;
 };
-__device__ __forceinline__ TileAt tile_at(int64_t u, const int* pb, int B, int G) {
-    int lo = 0, hi = B - 1;  // largest b with G * pb[b] <= u
+__device__ __forceinline__ TileAt tile_at(int x, const Sequences& q, int B, int G) {
+    int lo = 0, hi = B - 1;  // largest b with G * tiles[b] <= x
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)G * pb[mid] <= u) lo = mid; else hi = mid - 1;
+        if (G * q.tiles[mid] <= x) lo = mid; else hi = mid - 1;
     }
     TileAt t;
     t.b = lo;
-    const int nu = pb[lo + 1] - pb[lo];
-    const int64_t rel = u - (int64_t)G * pb[lo];
-    t.g = rel < INT32_MAX ? (int)rel / nu : (int)(rel / nu);
-    t.i = (int)(rel - (int64_t)t.g * nu) - kPieceTiles;
-    t.nt = nu - kPieceTiles;
+    t.nt = q.tiles[lo + 1] - q.tiles[lo];
+    const int rel = x - G * q.tiles[lo];
+    t.g = (int)((unsigned)rel / (unsigned)t.nt);
+    t.i = rel - t.g * t.nt;
     return t;
 }
+
+// Floats of one partial state: the output rows, then the heads' maxima and sums.
+__host__ __device__ __forceinline__ int state_floats(int r, int d) { return (r * d + 2 * r + 3) & ~3; }
 
 // D[16x8] = A[16x16] * B[16x8] + C, fp16 inputs.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -202,16 +243,30 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
 
-// The gate applied to one output value (e: feature).
+// The gate applied to one output value (e: feature), and to four neighbouring ones.
+__device__ __forceinline__ float gate_apply(int mode, float z, float o) {
+    const float a = gate_act(z, sigmoidf_dev(z), mode);
+    return gate_additive(mode) ? o + a : o * a;
+}
 __device__ __forceinline__ float gated(const QcacheDecodeParams& p, int b, int h, int e, float o) {
     const int layout = gate_layout(p.gate_mode);
     if (layout == GATTN_GATE_NONE) return o;
     const bf16* gp = static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride;
-    const float z = __bfloat162float(layout == GATTN_GATE_ELEMENTWISE ? gp[h * p.gate_head_stride + e]
-                                     : layout == GATTN_GATE_HEADWISE  ? gp[h * p.gate_head_stride]
-                                                                      : gp[e]);
-    const float a = gate_act(z, sigmoidf_dev(z), p.gate_mode);
-    return gate_additive(p.gate_mode) ? o + a : o * a;
+    return gate_apply(p.gate_mode,
+                      __bfloat162float(layout == GATTN_GATE_ELEMENTWISE ? gp[h * p.gate_head_stride + e]
+                                       : layout == GATTN_GATE_HEADWISE  ? gp[h * p.gate_head_stride]
+                                                                        : gp[e]),
+                      o);
+}
+__device__ __forceinline__ void gated4(const QcacheDecodeParams& p, int b, int h, int e, float (&o)[4]) {
+    const int layout = gate_layout(p.gate_mode);
+    if (layout == GATTN_GATE_NONE) return;
+    const bf16* gp = static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride;
+    if (layout != GATTN_GATE_HEAD_SHARED) gp += h * p.gate_head_stride;
+    const int step = layout == GATTN_GATE_HEADWISE ? 0 : 1;
+    if (step) gp += e;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = gate_apply(p.gate_mode, __bfloat162float(gp[k * step]), o[k]);
 }
 
 // The queries of one piece as B fragments (all threads).  A thread takes eight
@@ -312,8 +367,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     uint8_t* tail = smem + NW * n_stages * C::STAGE_BYTES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = p.H / p.G, Lmax = p.max_pages * p.page_size;
-    int* pb = reinterpret_cast<int*>(tail + C::OFF_OBUF + obuf_bytes<D>(r, p.rd));
-    int* lens = pb + p.B + 1;
+    const Sequences seqs(tail + C::OFF_OBUF + obuf_bytes<D>(r, p.rd), p.B);
     const uint32_t ring_u32 = smem_u32(smem) + warp * n_stages * C::STAGE_BYTES;
     uint8_t* ring = smem + warp * n_stages * C::STAGE_BYTES;
     const uint32_t bars = smem_u32(tail + C::OFF_BAR) + warp * 8 * C::MAX_STAGES;
@@ -325,15 +379,20 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         fence_mbar_init();
     }
     if (threadIdx.x == 0) *abort_flag = 0;
-    // rows of heads that do not exist stay zero
-    for (int i = threadIdx.x; i < C::OFF_ML / 4; i += THREADS) reinterpret_cast<uint32_t*>(tail)[i] = 0u;
-    unit_prefix<D>(p.seqlens, p.B, Lmax, pb, lens, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
+    // heads and (in the sums) groups that do not exist stay zero
+    for (int i = threadIdx.x + (r < 8 ? 0 : C::OFF_QSUM / 16); i < C::OFF_ML / 16; i += THREADS)
+        reinterpret_cast<uint4*>(tail)[i] = make_uint4(0, 0, 0, 0);
+    scan_batch<D>(p.seqlens, p.B, Lmax, seqs, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
 
-    const int64_t U = (int64_t)p.G * pb[p.B];
-    const int N = active_ctas(U, gridDim.x);
-    if (blockIdx.x >= N) return;
-    const int64_t u_begin = blockIdx.x * U / N;
-    const int n_units = (int)((blockIdx.x + 1) * U / N - u_begin);
+    const WorkSplit split(p.G * (seqs.tiles[p.B] + kPieceTiles * seqs.live[p.B]), gridDim.x);
+    if ((int)blockIdx.x >= split.N) return;
+    // this CTA's tiles: x0 .. x0 + n_tiles - 1 of the batch
+    int x0 = 0, n_tiles = 0;
+    {
+        const int x = tiles_ahead(split.start(blockIdx.x + (lane & 1)), seqs, p.B, p.G);
+        x0 = __shfl_sync(0xffffffffu, x, 0);
+        n_tiles = __shfl_sync(0xffffffffu, x, 1) - x0;
+    }
     const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * C::BLOCK_BYTES;
     const int bpp = p.page_size / kQcBlock;
     if (after_write) {  // the appended rows were written by the kernel before this one
@@ -341,29 +400,33 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         fence_proxy_async_global();
     }
 
-    // ---- the warp's copies run n_stages units ahead.  Lane j holds the addresses of the
-    // warp's blocks of unit 32 k + j (0: no tile, or past the sequence's end), 32 units'
-    // table entries a time.  A unit without a block still completes its stage's phase, so
-    // the stages' parities flip together.
-    int sent = 0, s_send = 0;
+    // ---- the warp's copies run n_stages tiles ahead.  Lane j holds the addresses of the
+    // warp's blocks of tile x0 + 32 k + j (0: past the sequence's end), 32 tiles' table
+    // entries a time.  A tile without a block for this warp still completes its stage's
+    // phase, so the stages' parities flip together.
+    int sent = 0;
     uint64_t src[C::NB] = {};
-    auto send = [&]() {  // all lanes; unit `sent` into stage s_send
-        if (sent >= n_units) return;
+    TileAt at = {};  // first the CTA's first tile, then the piece at hand
+    auto send = [&](int stage) {  // all lanes; tile x0 + sent into `stage`
+        if (sent >= n_tiles) return;
         if ((sent & 31) == 0) {
 #pragma unroll
             for (int j = 0; j < C::NB; ++j) src[j] = 0;
-            if (sent + lane < n_units) {
-                const TileAt t = tile_at(u_begin + sent + lane, pb, p.B, p.G);
+            const TileAt t = tile_at(x0 + min(sent + lane, n_tiles - 1), seqs, p.B, p.G);
+            if (sent == 0) at = TileAt{__shfl_sync(0xffffffffu, t.b, 0), __shfl_sync(0xffffffffu, t.g, 0),
+                                       __shfl_sync(0xffffffffu, t.i, 0), __shfl_sync(0xffffffffu, t.nt, 0)};
+            if (sent + lane < n_tiles) {
 #pragma unroll
                 for (int j = 0; j < C::NB; ++j) {
                     const int blk = (t.i * NW + warp) * C::NB + j;
-                    if (t.i >= 0 && blk * kQcBlock < lens[t.b]) {
-                        int page = p.block_table[(int64_t)t.b * p.max_pages + blk / bpp];
+                    if (blk * kQcBlock < seqs.lens[t.b]) {
+                        const int slot = page_of(blk, p.by_page);
+                        int page = p.block_table[(int64_t)t.b * p.max_pages + slot];
                         if (page < 0 || page >= p.num_pages) {
                             atomicOr(p.status, GATTN_DEVICE_BAD_PAGE);
                             page = 0;
                         }
-                        src[j] = reinterpret_cast<uint64_t>(p.cache + (((int64_t)page * p.G + t.g) * bpp + blk % bpp) * C::BLOCK_BYTES);
+                        src[j] = reinterpret_cast<uint64_t>(p.cache + (((int64_t)page * p.G + t.g) * bpp + (blk - slot * bpp)) * C::BLOCK_BYTES);
                     }
                 }
             }
@@ -372,31 +435,33 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 #pragma unroll
         for (int j = 0; j < C::NB; ++j) a[j] = __shfl_sync(0xffffffffu, src[j], sent & 31);
         if (elect_one()) {
-            const uint32_t bar = bars + 8 * s_send, dst = ring_u32 + s_send * C::STAGE_BYTES;
-            const uint8_t* k0 = reinterpret_cast<const uint8_t*>(a[0]);
-            if (C::NB == 2 && a[C::NB - 1] == a[0] + C::BLOCK_BYTES) {  // two blocks in a row
-                mbar_arrive_expect_tx(bar, 4 * C::BLOCK_BYTES);
-                bulk_load(dst, k0, 2 * C::BLOCK_BYTES, bar);
-                bulk_load(dst + 2 * C::BLOCK_BYTES, k0 + plane, 2 * C::BLOCK_BYTES, bar);
-            } else if (a[0]) {
-                const bool two = C::NB == 2 && a[C::NB - 1];
-                mbar_arrive_expect_tx(bar, (two ? 4 : 2) * C::BLOCK_BYTES);
-                bulk_load(dst, k0, C::BLOCK_BYTES, bar);
-                bulk_load(dst + C::NB * C::BLOCK_BYTES, k0 + plane, C::BLOCK_BYTES, bar);
-                if (two) {
-                    const uint8_t* k1 = reinterpret_cast<const uint8_t*>(a[C::NB - 1]);
-                    bulk_load(dst + C::BLOCK_BYTES, k1, C::BLOCK_BYTES, bar);
-                    bulk_load(dst + (C::NB + 1) * C::BLOCK_BYTES, k1 + plane, C::BLOCK_BYTES, bar);
-                }
+            const uint32_t bar = bars + 8 * stage, dst = ring_u32 + stage * C::STAGE_BYTES;
+            bool row = true;  // the blocks lie in a row: one copy a plane
+            int n = a[0] != 0;
+#pragma unroll
+            for (int j = 1; j < C::NB; ++j) {
+                row = row && a[j] == a[0] + j * C::BLOCK_BYTES;
+                n += a[j] != 0;
+            }
+            if (row && a[0]) {
+                mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+                bulk_load(dst, reinterpret_cast<const uint8_t*>(a[0]), C::NB * C::BLOCK_BYTES, bar);
+                bulk_load(dst + C::NB * C::BLOCK_BYTES, reinterpret_cast<const uint8_t*>(a[0]) + plane,
+                          C::NB * C::BLOCK_BYTES, bar);
             } else {
-                mbar_arrive(bar);
+                mbar_arrive_expect_tx(bar, 2 * n * C::BLOCK_BYTES);
+#pragma unroll
+                for (int j = 0; j < C::NB; ++j) {
+                    if (!a[j]) continue;
+                    const uint8_t* k = reinterpret_cast<const uint8_t*>(a[j]);
+                    bulk_load(dst + j * C::BLOCK_BYTES, k, C::BLOCK_BYTES, bar);
+                    bulk_load(dst + (C::NB + j) * C::BLOCK_BYTES, k + plane, C::BLOCK_BYTES, bar);
+                }
             }
         }
-        __syncwarp();
         ++sent;
-        if (++s_send == n_stages) s_send = 0;
     };
-    for (int s = 0; s < n_stages; ++s) send();
+    for (int s = 0; s < n_stages; ++s) send(s);
 
     const int gid = lane >> 2, t = lane & 3;
     // V words are read so that the four lanes of a quad touch different banks: the upper
@@ -417,23 +482,16 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     };
     auto release = [&]() {  // the warp is through with the stage: the next copy goes there
         __syncwarp();
-        if (!dead) send();
+        if (!dead) send(st);
         if (++st == n_stages) {
             st = 0;
             phase ^= 1u;
         }
     };
-    TileAt at = tile_at(u_begin, pb, p.B, p.G);
-    for (int n = 0; n < n_units;) {
-        const int i1 = min(at.nt, at.i + (n_units - n));  // this CTA's tiles of the piece: [i0, i1)
-        const int i0 = max(at.i, 0);
-        const int L = lens[at.b];
-        n += i1 - at.i;
-        for (int i = at.i; i < min(i0, i1); ++i) {  // the piece's own units hold no tile
-            receive();
-            release();
-        }
-        if (i1 <= 0) break;
+    for (int n = 0; n < n_tiles;) {
+        const int i0 = at.i, i1 = min(at.nt, i0 + (n_tiles - n));  // this CTA's tiles of the piece
+        const int L = seqs.lens[at.b];
+        n += i1 - i0;
         const bool alone = i0 == 0 && i1 == at.nt;
         make_queries<D>(p, at.b, at.g, L - 1, tail);
         const float2 qsc = ld<float2>(tail + C::OFF_QSC + t * 8);
@@ -673,28 +731,32 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
             __syncthreads();
         }
         const float2* tot = reinterpret_cast<const float2*>(tail + C::OFF_TOT);
-        const int h0 = at.g * r;
         if (alone) {
-            for (int j = threadIdx.x; j < r * D; j += THREADS) {
+            bf16* out = static_cast<bf16*>(p.out) + ((int64_t)at.b * p.H + at.g * r) * D;
+            for (int j = 4 * threadIdx.x; j < r * D; j += 4 * THREADS) {
                 const int h = j / D, e = j % D;
-                static_cast<bf16*>(p.out)[((int64_t)at.b * p.H + h0) * D + j] =
-                    __float2bfloat16_rn(gated(p, at.b, h0 + h, e, obuf[h * C::OROW + e] / tot[h].y));
+                const float4 o = *reinterpret_cast<const float4*>(obuf + h * C::OROW + e);
+                const float l = 1.f / tot[h].y;
+                float v[4] = {o.x * l, o.y * l, o.z * l, o.w * l};
+                gated4(p, at.b, at.g * r + h, e, v);
+                *reinterpret_cast<uint2*>(out + j) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
             }
         } else {
-            float* ps = p.part + ((int64_t)blockIdx.x + (int64_t)at.b * p.G + at.g) * (int64_t)(2 * r + r * D);
-            for (int j = threadIdx.x; j < r * D; j += THREADS) ps[2 * r + j] = obuf[(j / D) * C::OROW + j % D];
+            float* ps = p.part + ((int64_t)blockIdx.x + (int64_t)at.b * p.G + at.g) * state_floats(r, D);
+            for (int j = 4 * threadIdx.x; j < r * D; j += 4 * THREADS)
+                *reinterpret_cast<float4*>(ps + j) = *reinterpret_cast<const float4*>(obuf + (j / D) * C::OROW + j % D);
             if (threadIdx.x < r) {
-                ps[threadIdx.x] = tot[threadIdx.x].x;
-                ps[r + threadIdx.x] = tot[threadIdx.x].y;
+                ps[r * D + threadIdx.x] = tot[threadIdx.x].x;
+                ps[r * D + r + threadIdx.x] = tot[threadIdx.x].y;
             }
         }
         // the next piece: the next KV head, or the next sequence that holds anything
-        at.i = -kPieceTiles;
+        at.i = 0;
         if (++at.g == p.G) {
             at.g = 0;
-            do { ++at.b; } while (at.b < p.B && pb[at.b + 1] == pb[at.b]);
+            do { ++at.b; } while (at.b < p.B && seqs.tiles[at.b + 1] == seqs.tiles[at.b]);
             if (at.b == p.B) break;
-            at.nt = pb[at.b + 1] - pb[at.b] - kPieceTiles;
+            at.nt = seqs.tiles[at.b + 1] - seqs.tiles[at.b];
         }
     }
     // every copy that was sent lands before the block leaves (none is left unless a wait ran out)
@@ -713,11 +775,11 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
     const int r = p.H / p.G, g = hq / r, h = hq % r, Lmax = p.max_pages * p.page_size;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = p.seqlens[b], nt = seq_tiles<D>(L, Lmax);
-    int before = 0, total = 0;  // units ahead of this sequence, and of all
+    int before = 0, total = 0;  // units ahead of this sequence, and of all (one KV head)
     for (int i = threadIdx.x; i < p.B; i += 32 * NWC) {
-        const int n = seq_units<D>(p.seqlens[i], Lmax);
-        total += n;
-        if (i < b) before += n;
+        const int n = seq_tiles<D>(p.seqlens[i], Lmax), u = n ? n + kPieceTiles : 0;
+        total += u;
+        if (i < b) before += u;
     }
     before = __reduce_add_sync(0xffffffffu, before);
     total = __reduce_add_sync(0xffffffffu, total);
@@ -735,14 +797,12 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
     bf16* out = static_cast<bf16*>(p.out) + ((int64_t)b * p.H + hq) * D;
     int n_slots = 0, c0 = 0;
     if (nt) {
-        const int64_t U = (int64_t)p.G * total;
-        const int N = active_ctas(U, n_ctas);
-        const int64_t u0 = (int64_t)p.G * before + (int64_t)g * (nt + kPieceTiles) + kPieceTiles, u1 = u0 + nt - 1;
-        // CTA c holds units [c U / N, (c + 1) U / N): the ones that hold the first and the last tile
-        c0 = (int)(((u0 + 1) * N - 1) / U);
-        n_slots = (int)(((u1 + 1) * N - 1) / U) - c0 + 1;
+        const WorkSplit split(p.G * total, n_ctas);
+        const int u0 = p.G * before + g * (nt + kPieceTiles) + kPieceTiles;  // the first tile's unit
+        c0 = split.owner(u0);
+        n_slots = split.owner(u0 + nt - 1) - c0 + 1;
     }
-    const int64_t stride = 2 * r + r * D;
+    const int64_t stride = state_floats(r, D);
     const float* part0 = p.part + ((int64_t)c0 + (int64_t)b * p.G + g) * stride;
 
     // Everything above reads only the inputs.  Every block waits for the split kernel before
@@ -767,10 +827,10 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
             const int s = s0 + j * NWC;
             const bool live = s < n_slots;
             const float* ps = part0 + (live ? s : 0) * stride;
-            ms[j] = live ? ps[h] : -INFINITY;
-            ls[j] = live ? ps[r + h] : 0.f;
+            ms[j] = live ? ps[r * D + h] : -INFINITY;
+            ls[j] = live ? ps[r * D + r + h] : 0.f;
 #pragma unroll
-            for (int k = 0; k < DPL; ++k) os[j][k] = live ? ps[2 * r + h * D + lane + 32 * k] : 0.f;
+            for (int k = 0; k < DPL; ++k) os[j][k] = live ? ps[h * D + lane + 32 * k] : 0.f;
         }
         float mx = m_run;
 #pragma unroll
@@ -856,7 +916,7 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
 size_t qcache_decode_workspace(int B, int H, int G, int d, int n_sms) {
     const int per_sm = d == 256 ? QdCfg<256>::CTAS_PER_SM : QdCfg<64>::CTAS_PER_SM;
     const int r = H / G;
-    return ((size_t)per_sm * n_sms + (size_t)B * G) * (size_t)(2 * r + r * d) * sizeof(float);
+    return ((size_t)per_sm * n_sms + (size_t)B * G) * (size_t)state_floats(r, d) * sizeof(float);
 }
 
 cudaError_t launch_qcache_decode(const QcacheDecodeParams& p, bool after_write, cudaStream_t stream,

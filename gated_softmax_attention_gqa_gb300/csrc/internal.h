@@ -143,7 +143,8 @@ gattn_status decode_check_args(const void* q_new, const void* kv_cache, const in
                                const void* qnorm_w, int B, int H, int G, int d, int Lmax, int rotary_dim,
                                double rope_base, float eps, int gate_mode, const void* out, int64_t cache_rows);
 
-// Division by page_size of a token index below 2^31: (x * mul) >> 32 >> shift.
+// Division of an index below 2^31 by a page's tokens or blocks: (x * mul) >> 32 >> shift, or
+// x itself where mul is 0.
 struct PageDiv {
     uint32_t mul, shift;
 };
@@ -188,6 +189,7 @@ struct QcacheDecodeParams {
     float* part;  // partial softmax states
     int64_t q_seq_stride, q_head_stride, gate_seq_stride, gate_head_stride;
     int num_pages, page_size, max_pages;
+    PageDiv by_page;  // divides a block index by the blocks of a page
     int B, H, G, d, rd, gate_mode, n_sms;
     float eps, scale_log2;
     unsigned int* status;

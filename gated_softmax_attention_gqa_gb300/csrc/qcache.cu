@@ -107,7 +107,7 @@ enum { kSkip = 0, kLive = 1, kBadLength = 2, kBadPage = 3 };
 
 template <typename P>
 __device__ __forceinline__ int find_page(const P& p, int b, Place& at) {
-    const int k = (int)(__umulhi((uint32_t)at.pos, p.by_page.mul) >> p.by_page.shift);
+    const int k = page_of(at.pos, p.by_page);
     at.slot = at.pos - k * p.page_size;
     at.page = p.block_table[(int64_t)b * p.max_pages + k];
     return at.page >= 0 && at.page < p.num_pages ? kLive : kBadPage;

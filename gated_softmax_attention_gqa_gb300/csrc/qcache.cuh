@@ -31,6 +31,10 @@ __device__ __forceinline__ int64_t qc_block_offset(int page, int g, int slot, in
     return (((int64_t)page * G + g) * (page_size / kQcBlock) + slot / kQcBlock) * qc_block_bytes(d);
 }
 
+__device__ __forceinline__ int page_of(int x, const PageDiv& d) {
+    return d.mul ? (int)(__umulhi((uint32_t)x, d.mul) >> d.shift) : x;
+}
+
 // max / min that return NaN when any operand is one
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;

@@ -36,7 +36,9 @@ void fill_turns(uint64_t* dst, int rd, double base) {
 
 // floor(x / d) = floor(x m / 2^(31 + k)) for 0 <= x < 2^31, with 2^k the power of two at or
 // above d >= 2 and m = floor(2^(31 + k) / d) + 1 (m d exceeds 2^(31 + k) by at most d <= 2^k).
+// mul = 0 stands for d = 1.
 PageDiv page_div(int d) {
+    if (d == 1) return PageDiv{0, 0};
     int k = 0;
     while (((int64_t)1 << k) < d) ++k;
     return PageDiv{(uint32_t)((((uint64_t)1 << (31 + k)) / (uint64_t)d) + 1), (uint32_t)(k - 1)};
@@ -221,6 +223,7 @@ gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const voi
     p.num_pages = num_pages;
     p.page_size = page_size;
     p.max_pages = max_pages;
+    p.by_page = page_div(page_size / kQcBlock);
     p.B = B;
     p.H = H;
     p.G = G;
