@@ -395,11 +395,6 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     }
     const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * C::BLOCK_BYTES;
     const int bpp = p.page_size / kQcBlock;
-    if (after_write) {  // the appended rows were written by the kernel before this one
-        pdl_wait_prerequisites();
-        fence_proxy_async_global();
-    }
-
     // ---- the warp's copies run n_stages tiles ahead.  Lane j holds the addresses of the
     // warp's blocks of tile x0 + 32 k + j (0: past the sequence's end), 32 tiles' table
     // entries a time.  A tile without a block for this warp still completes its stage's
@@ -430,6 +425,10 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     }
                 }
             }
+        }
+        if (sent == 0 && after_write) {  // the appended rows are being written by the kernel before this one
+            pdl_wait_prerequisites();
+            fence_proxy_async_global();
         }
         uint64_t a[C::NB];
 #pragma unroll

@@ -69,6 +69,8 @@ struct Row16<float> {
     }
 };
 
+__device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The codes of eight features (four pairs), lowest feature in the lowest nibble.  CLAMP is
@@ -87,9 +89,9 @@ __device__ __forceinline__ uint32_t encode8(const float2* p, const QcGroup& g) {
                 u[i] = make_float2(fminf(fmaxf(u[i].x, kQcMagic), kQcMagic + 15.f),
                                    fminf(fmaxf(u[i].y, kQcMagic), kQcMagic + 15.f));
         }
-        // magic + even code + 16 odd code: a byte in the low mantissa bits
-        const float2 b = fma2(add2(u[1], both(-kQcMagic)), both(16.f), u[0]);
-        h[q] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+        // the bits of magic + code end in the code: even + 16 odd is a byte, garbage above it
+        h[q] = __byte_perm(__float_as_uint(u[0].x) + 16u * __float_as_uint(u[1].x),
+                           __float_as_uint(u[0].y) + 16u * __float_as_uint(u[1].y), 0x0040);
     }
     return __byte_perm(h[0], h[1], 0x5410);
 }
@@ -189,34 +191,35 @@ __device__ __forceinline__ void encode_store(const Vec16& x, uint8_t* block, int
         (uint16_t)(j ? q.bits >> 16 : q.bits);
 }
 
-// A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass of a warp; a warp
-// takes `passes` of them and walks heads [blockIdx.y heads, ...) in each.
-template <int D, typename T>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
+// A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass.  `TEAM` of the block's
+// warps (one or all) take the same tokens, `passes` passes of them, and every TEAM-th of the
+// heads [blockIdx.y heads, ...); they make the sines and cosines together.
+template <int D, typename T, int TEAM>
+__global__ void __launch_bounds__(32 * kWarps, 4)
     qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
-    __shared__ __align__(16) float2 tables[kWarps][TPW * D / 2 + 8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t0 = (blockIdx.x * kWarps + warp) * TPW * passes;
-    if (t0 >= p.T) return;
-    const int e0 = 16 * (lane % LPR), g0 = blockIdx.y * heads, n_heads = min(p.G, g0 + heads) - g0;
+    // sines and cosines of a pass, {sin, cos} of frequencies 2u, 2u + 1 in element
+    // [token][u % 4][u / 4] (lanes of neighbouring features read neighbouring elements), and one
+    // element that turns nothing
+    __shared__ float4 tables[kWarps / TEAM][TPW * D / 4 + 1];
+    // norm weights, and the rotation partners' with the rotation's sign, in Vec16 order
+    __shared__ float4 weights[2][4][LPR];
+    pdl_launch_dependents();  // a decode step may set itself up; it waits for this grid before it reads the cache
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mate_id = warp % TEAM, tl = lane / LPR, lc = lane % LPR;
+    const int t0 = (blockIdx.x * (kWarps / TEAM) + warp / TEAM) * TPW * passes;
+    const int e0 = 16 * lc, g0 = blockIdx.y * heads + mate_id, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
     const int half = p.rd >> 1;
-    // rotation partners, eight features at a time (half is a multiple of 8); features past
-    // rotary_dim are their own, turned by nothing (entries half .. half + 7 of a table)
-    int mate[2], turn[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int e = e0 + 8 * c;
-        mate[c] = e < half ? half : e < p.rd ? -half : 0;
-        turn[c] = e < half ? e : e - half;
-    }
+    // distance of the rotation partner, eight features at a time (half is a multiple of 8);
+    // 0: features past rotary_dim, which are not turned
+    auto partner = [&](int e) { return e < half ? half : e < p.rd ? -half : 0; };
+    const int mate[2] = {partner(e0), partner(e0 + 8)};
     const T* kp;
     const T* vp;
     Row16<T> kr, ko, vr;
     auto start = [&](int pass) {  // the first head's rows of a pass
-        const int64_t t = min(t0 + pass * TPW + lane / LPR, p.T - 1);
-        kp = static_cast<const T*>(p.k) + t * p.k_tok_stride + g0 * p.k_head_stride + e0;
-        vp = static_cast<const T*>(p.v) + t * p.v_tok_stride + g0 * p.v_head_stride + e0;
+        const int64_t t = min(t0 + pass * TPW + tl, p.T - 1), g = min(g0, p.G - 1);
+        kp = static_cast<const T*>(p.k) + t * p.k_tok_stride + g * p.k_head_stride + e0;
+        vp = static_cast<const T*>(p.v) + t * p.v_tok_stride + g * p.v_head_stride + e0;
     };
     auto load_k = [&]() {
         kr.load(kp);
@@ -232,59 +235,62 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     const bool ok = report(lane < passes * TPW ? place_new(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
 
-    float2* table = tables[warp];
-    const float2* sc[2];
+    for (int e = threadIdx.x; e < D; e += 32 * kWarps) {
+        const int m = partner(e), at = (((e >> 2) & 3) * LPR + (e >> 4)) * 4 + (e & 1) * 2 + ((e >> 1) & 1);
+        const T* w = static_cast<const T*>(p.knorm_w);
+        reinterpret_cast<float*>(weights[0])[at] = to_float(w[e]);
+        reinterpret_cast<float*>(weights[1])[at] = m > 0 ? -to_float(w[e + m]) : to_float(w[e + m]);
+    }
+    float4* table = tables[warp / TEAM];
+    if (lane == 0) table[TPW * D / 4] = make_float4(0.f, 1.f, 0.f, 1.f);
+    const float4* sc[2];
+    int step[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) sc[c] = table + (mate[c] ? (lane / LPR) * half + turn[c] : TPW * half);
-    if (lane < 8) table[TPW * half + lane] = make_float2(0.f, 1.f);
+    for (int c = 0; c < 2; ++c) {
+        const int e = e0 + 8 * c;
+        sc[c] = table + (mate[c] ? tl * (half / 2) + (e < half ? e : e - half) / 8 : TPW * D / 4);
+        step[c] = mate[c] ? half / 8 : 0;
+    }
     const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
+    __syncthreads();
 
     for (int pass = 0; pass < passes; ++pass) {
-        if (t0 + pass * TPW >= p.T) break;
-        // sines and cosines of the pass's tokens
-        __syncwarp();
-        for (int k = 0; k < TPW; ++k) {
+        if (TEAM == 1 && t0 + pass * TPW >= p.T) break;
+        for (int k = mate_id; k < TPW; k += TEAM) {
             const int pos = __shfl_sync(0xffffffffu, mine.pos, pass * TPW + k);
             for (int i = lane; i < half; i += 32) {
                 float s, c;
                 rope_turn_sincos(p.turns[i], pos, &s, &c);
-                table[k * half + i] = make_float2(s, c);
+                reinterpret_cast<float2*>(table + k * (half / 2) + ((i >> 1) & 3) * (half / 8) + (i >> 3))[i & 1] =
+                    make_float2(s, c);
             }
         }
-        __syncwarp();
+        if (TEAM > 1) __syncthreads(); else __syncwarp();
         // K' = (x wc + partner ws) / rms
         Vec16 wc, ws;
-        {
-            Row16<T> wr;
-            wr.load(static_cast<const T*>(p.knorm_w) + e0);
-            wr.get(wc);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) wr.load8(c, static_cast<const T*>(p.knorm_w) + e0 + 8 * c + mate[c]);
-            wr.get(ws);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {  // the partner of a first half's feature enters with -sin
-                const float4 a = *reinterpret_cast<const float4*>(sc[q >> 1] + 4 * (q & 1));
-                const float4 b = *reinterpret_cast<const float4*>(sc[q >> 1] + 4 * (q & 1) + 2);
-                const float2 sign = both(mate[q >> 1] > 0 ? -1.f : 1.f);
-                wc.p[2 * q] = mul2(wc.p[2 * q], make_float2(a.y, b.y));
-                wc.p[2 * q + 1] = mul2(wc.p[2 * q + 1], make_float2(a.w, b.w));
-                ws.p[2 * q] = mul2(ws.p[2 * q], mul2(make_float2(a.x, b.x), sign));
-                ws.p[2 * q + 1] = mul2(ws.p[2 * q + 1], mul2(make_float2(a.z, b.z), sign));
-            }
+        for (int q = 0; q < 4; ++q) {
+            const float4 w = weights[0][q][lc], m = weights[1][q][lc];
+            const float4 a = sc[q >> 1][(2 * q & 3) * step[q >> 1]], b = sc[q >> 1][((2 * q & 3) + 1) * step[q >> 1]];
+            wc.p[2 * q] = mul2(make_float2(w.x, w.y), make_float2(a.y, b.y));
+            wc.p[2 * q + 1] = mul2(make_float2(w.z, w.w), make_float2(a.w, b.w));
+            ws.p[2 * q] = mul2(make_float2(m.x, m.y), make_float2(a.x, b.x));
+            ws.p[2 * q + 1] = mul2(make_float2(m.z, m.w), make_float2(a.z, b.z));
         }
-        const Place at = place_of(mine, pass * TPW + lane / LPR);
+        if (TEAM > 1) __syncthreads(); else __syncwarp();  // the next pass overwrites the table
+        const Place at = place_of(mine, pass * TPW + tl);
         const bool live = at.page >= 0;
         uint8_t* block = p.cache + (live ? (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) : 0);
         const int row = at.slot % kQcBlock;
-        for (int g = 0; g < n_heads; ++g) {
+        for (int g = g0; g < g1; g += TEAM) {
             vr.load(vp);
-            vp += p.v_head_stride;
+            vp += TEAM * p.v_head_stride;
             Vec16 x, o;
             kr.get(x);
             ko.get(o);
             // the next K rows: the next head's, or the next pass's first
-            if (g + 1 < n_heads) {
-                kp += p.k_head_stride;
+            if (g + TEAM < g1) {
+                kp += TEAM * p.k_head_stride;
                 load_k();
             } else if (pass + 1 < passes) {
                 start(pass + 1);
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
             encode_store(x, block, row, e0, D, live);
             vr.get(x);
             encode_store(x, block + plane, row, e0, D, live);
-            block += head;
+            block += TEAM * head;
         }
     }
 }
@@ -335,12 +341,12 @@ __device__ __forceinline__ void decode8(uint32_t n, uint32_t s2, uint32_t c2, fl
 // The same layout of work: a lane reads back 16 features of one token, head after head.
 template <int D, typename T>
 __global__ void __launch_bounds__(32 * kWarps)
-    qcache_read_kernel(const __grid_constant__ QcacheReadParams p, int passes, int heads) {
+    qcache_read_kernel(const __grid_constant__ QcacheReadParams p, int passes, int heads, int team) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t0 = (blockIdx.x * kWarps + warp) * TPW * passes;
-    if (t0 >= p.T) return;
-    const int e0 = 16 * (lane % LPR), g0 = blockIdx.y * heads, n_heads = min(p.G, g0 + heads) - g0;
+    const int t0 = (blockIdx.x * (kWarps / team) + warp / team) * TPW * passes;
+    const int e0 = 16 * (lane % LPR), g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
+    if (t0 >= p.T || g0 >= g1) return;
     Place mine;  // of token t0 + lane
     const bool ok = report(lane < passes * TPW ? place_cached(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(32 * kWarps)
         T* kout = static_cast<T*>(p.k) + (t * p.G + g0) * D + e0;
         T* vout = static_cast<T*>(p.v) + (t * p.G + g0) * D + e0;
 #pragma unroll 4
-        for (int g = 0; g < n_heads; ++g) {
+        for (int g = g0; g < g1; g += team) {
             uint4 w[2];
             uint32_t s[2], c[2];
 #pragma unroll
@@ -374,28 +380,29 @@ __global__ void __launch_bounds__(32 * kWarps)
                 decode8(__byte_perm(w[i].x, w[i].y, sel), s2, c2, out);
                 decode8(__byte_perm(w[i].z, w[i].w, sel), s2, c2, out + 8);
             }
-            src += head;
-            kout += D;
-            vout += D;
+            src += team * head;
+            kout += team * D;
+            vout += team * D;
         }
     }
 }
 
-// How a call is cut: passes a warp takes (their lookups go together) and KV heads.  Both
-// shrink while they leave the device short of warps, as for a few tokens of a decode step.
+// How a call is cut: passes a warp takes (their lookups go together), KV heads of a block,
+// warps that share a token's heads.  A call too small to fill the device with one warp for
+// all heads of its tokens takes one pass and spreads the heads, over a block's warps first.
 struct Cut {
-    int passes, heads;
+    int passes, heads, team;
     dim3 grid;
 };
 template <int D>
 Cut cut_of(int T, int G) {
     constexpr int TPW = 32 / (D / 16);
-    const int64_t want = 16 * (int64_t)device_sm_count();
-    Cut c{2, G, dim3()};
-    auto warps = [&]() { return ((int64_t)T + TPW * c.passes - 1) / (TPW * c.passes) * ((G + c.heads - 1) / c.heads); };
-    while (c.passes > 1 && warps() < want) c.passes /= 2;
-    while (c.heads > 1 && warps() < want) c.heads = (c.heads + 1) / 2;
-    const int tokens = kWarps * TPW * c.passes;
+    const int64_t want = 8 * (int64_t)device_sm_count(), groups = ((int64_t)T + TPW - 1) / TPW;
+    Cut c{2, G, 1, dim3()};
+    if (groups < 2 * want) c.passes = 1;
+    if (G > 1 && groups < want) c.team = kWarps;
+    while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < want) c.heads = (c.heads + 1) / 2;
+    const int tokens = kWarps / c.team * TPW * c.passes;
     c.grid = dim3((unsigned)((T + tokens - 1) / tokens), (unsigned)((G + c.heads - 1) / c.heads));
     return c;
 }
@@ -403,16 +410,17 @@ Cut cut_of(int T, int G) {
 template <int D>
 cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) {
     const Cut c = cut_of<D>(p.T, p.G);
-    if (fp32) qcache_write_kernel<D, float><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
-    else qcache_write_kernel<D, bf16><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
+    auto kernel = fp32 ? (c.team > 1 ? qcache_write_kernel<D, float, kWarps> : qcache_write_kernel<D, float, 1>)
+                       : (c.team > 1 ? qcache_write_kernel<D, bf16, kWarps> : qcache_write_kernel<D, bf16, 1>);
+    kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t read_d(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
     const Cut c = cut_of<D>(p.T, p.G);
-    if (fp32) qcache_read_kernel<D, float><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
-    else qcache_read_kernel<D, bf16><<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
+    auto kernel = fp32 ? qcache_read_kernel<D, float> : qcache_read_kernel<D, bf16>;
+    kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads, c.team);
     return cudaGetLastError();
 }
 
