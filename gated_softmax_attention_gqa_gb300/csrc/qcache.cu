@@ -16,9 +16,15 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// Sixteen consecutive features, in pairs for the two-wide fp32 instructions: quad q's
-// features 4q, 4q + 2 in p[2q] and 4q + 1, 4q + 3 in p[2q + 1], so that a quad's codes
-// combine pair by pair too.
+// A lane's sixteen features of a group of 32 are two runs of eight, 16 apart: its
+// neighbour (lane ^ 1) has the runs between, so that each 16-byte load or store of the two
+// fills whole 32-byte sectors.  (With sixteen in a row every sector passed twice, and the L1
+// path, 79% busy, held the write at 104 us where it moves 333 MB.)
+__device__ __forceinline__ int first_feature(int lane_of_token) { return 32 * (lane_of_token >> 1) + 8 * (lane_of_token & 1); }
+
+// The sixteen, in pairs for the two-wide fp32 instructions: of each four neighbours
+// (quad q) the first and third in p[2q], the second and fourth in p[2q + 1], so that a
+// quad's codes combine pair by pair too.
 struct Vec16 {
     float2 p[8];
 };
@@ -30,11 +36,7 @@ template <>
 struct Row16<bf16> {
     uint4 v[2];
     __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const bf16* p) {
-        v[0] = reinterpret_cast<const uint4*>(p)[0];
-        v[1] = reinterpret_cast<const uint4*>(p)[1];
-    }
-    // features 8 c .. 8 c + 7 only, from p
+    // run c (0 or 1) from p
     __device__ __forceinline__ void load8(int c, const bf16* p) { v[c] = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void get(Vec16& x) const {
 #pragma unroll
@@ -52,10 +54,6 @@ template <>
 struct Row16<float> {
     float4 v[4];
     __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = v[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void load(const float* p) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const float4*>(p)[i];
-    }
     __device__ __forceinline__ void load8(int c, const float* p) {
         v[2 * c] = reinterpret_cast<const float4*>(p)[0];
         v[2 * c + 1] = reinterpret_cast<const float4*>(p)[1];
@@ -159,7 +157,7 @@ __device__ __forceinline__ bool report(int what, unsigned int* status) {
 
 // Quantise this lane's 16 features (two neighbouring lanes share a group of 32, four a
 // slab) and store them at row `row` of `block`.  All lanes of the warp.
-__device__ __forceinline__ void encode_store(const Vec16& x, uint8_t* block, int row, int e0, int d, bool live) {
+__device__ __forceinline__ void encode_store(const Vec16& x, uint8_t* block, int row, int lc, int d, bool live) {
     float hi = max_nan(x.p[0].x, x.p[0].y), lo = min_nan(x.p[0].x, x.p[0].y);
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
@@ -178,24 +176,24 @@ __device__ __forceinline__ void encode_store(const Vec16& x, uint8_t* block, int
         w[0] = encode8<true>(x.p, q);
         w[1] = encode8<true>(x.p + 4, q);
     }
-    // lanes j and j + 2 of a slab hold features 16 j .. and 32 + 16 j ..: together the words
-    // 4 j .. 4 j + 3, of which lane j stores the first two and lane j + 2 the others
-    const int j = (e0 >> 4) & 1, upper = (e0 >> 5) & 1;
+    // lanes j and j ^ 2 of a slab hold the same features of its two groups, which meet in the
+    // words of both runs; the first group's lane stores the words of run 0, the other run 1's
+    const int odd = lc & 1, upper = (lc >> 1) & 1;
     const uint32_t o = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[1], 2);
     if (!live) return;
     const uint32_t a = upper ? o : w[0], b = upper ? w[1] : o;
-    *reinterpret_cast<uint2*>(block + (e0 >> 6) * 512 + row * 32 + 16 * j + 8 * upper) =
+    *reinterpret_cast<uint2*>(block + (lc >> 2) * 512 + row * 32 + 16 * upper + 8 * odd) =
         make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     // the group's two lanes store its scale and its centre
-    reinterpret_cast<uint16_t*>(block + 8 * d)[j * (d / 2) + (e0 >> 5) * 16 + row] =
-        (uint16_t)(j ? q.bits >> 16 : q.bits);
+    reinterpret_cast<uint16_t*>(block + 8 * d)[odd * (d / 2) + (lc >> 1) * 16 + row] =
+        (uint16_t)(odd ? q.bits >> 16 : q.bits);
 }
 
 // A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass.  `TEAM` of the block's
 // warps (one or all) take the same tokens, `passes` passes of them, and every TEAM-th of the
 // heads [blockIdx.y heads, ...); they make the sines and cosines together.
 template <int D, typename T, int TEAM>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 4)
     qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     // sines and cosines of a pass, {sin, cos} of frequencies 2u, 2u + 1 in element
@@ -204,39 +202,27 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     __shared__ float4 tables[kWarps / TEAM][TPW * D / 4 + 1];
     // norm weights, and the rotation partners' with the rotation's sign, in Vec16 order
     __shared__ float4 weights[2][4][LPR];
+    // their products with cosine and sine for the pass's tokens: each lane's own 32 floats,
+    // here rather than in registers, because the kernel lives on warps per SM (with 16 of them
+    // it moved 2.9 TB/s, whatever the instructions per warp)
+    __shared__ float4 factors[kWarps][8][32];
     pdl_launch_dependents();  // a decode step may set itself up; it waits for this grid before it reads the cache
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mate_id = warp % TEAM, tl = lane / LPR, lc = lane % LPR;
     const int t0 = (blockIdx.x * (kWarps / TEAM) + warp / TEAM) * TPW * passes;
-    const int e0 = 16 * lc, g0 = blockIdx.y * heads + mate_id, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
+    const int e0 = first_feature(lc), g0 = blockIdx.y * heads + mate_id, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
     const int half = p.rd >> 1;
     // distance of the rotation partner, eight features at a time (half is a multiple of 8);
     // 0: features past rotary_dim, which are not turned
     auto partner = [&](int e) { return e < half ? half : e < p.rd ? -half : 0; };
-    const int mate[2] = {partner(e0), partner(e0 + 8)};
-    const T* kp;
-    const T* vp;
-    Row16<T> kr, ko, vr;
-    auto start = [&](int pass) {  // the first head's rows of a pass
-        const int64_t t = min(t0 + pass * TPW + tl, p.T - 1), g = min(g0, p.G - 1);
-        kp = static_cast<const T*>(p.k) + t * p.k_tok_stride + g * p.k_head_stride + e0;
-        vp = static_cast<const T*>(p.v) + t * p.v_tok_stride + g * p.v_head_stride + e0;
-    };
-    auto load_k = [&]() {
-        kr.load(kp);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            if (mate[c]) ko.load8(c, kp + 8 * c + mate[c]);
-    };
-    start(0);
-    ko.zero();
-    load_k();
-
+    const int mate[2] = {partner(e0), partner(e0 + 16)};
     Place mine;  // of token t0 + lane
     const bool ok = report(lane < passes * TPW ? place_new(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
 
     for (int e = threadIdx.x; e < D; e += 32 * kWarps) {
-        const int m = partner(e), at = (((e >> 2) & 3) * LPR + (e >> 4)) * 4 + (e & 1) * 2 + ((e >> 1) & 1);
+        // run, quad and place of feature e in its lane's Vec16
+        const int m = partner(e), q = 2 * ((e >> 4) & 1) + ((e >> 2) & 1), of = 2 * (e >> 5) + ((e >> 3) & 1);
+        const int at = (q * LPR + of) * 4 + (e & 1) * 2 + ((e >> 1) & 1);
         const T* w = static_cast<const T*>(p.knorm_w);
         reinterpret_cast<float*>(weights[0])[at] = to_float(w[e]);
         reinterpret_cast<float*>(weights[1])[at] = m > 0 ? -to_float(w[e + m]) : to_float(w[e + m]);
@@ -247,7 +233,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     int step[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const int e = e0 + 8 * c;
+        const int e = e0 + 16 * c;
         sc[c] = table + (mate[c] ? tl * (half / 2) + (e < half ? e : e - half) / 8 : TPW * D / 4);
         step[c] = mate[c] ? half / 8 : 0;
     }
@@ -267,35 +253,38 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
         }
         if (TEAM > 1) __syncthreads(); else __syncwarp();
         // K' = (x wc + partner ws) / rms
-        Vec16 wc, ws;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float4 w = weights[0][q][lc], m = weights[1][q][lc];
             const float4 a = sc[q >> 1][(2 * q & 3) * step[q >> 1]], b = sc[q >> 1][((2 * q & 3) + 1) * step[q >> 1]];
-            wc.p[2 * q] = mul2(make_float2(w.x, w.y), make_float2(a.y, b.y));
-            wc.p[2 * q + 1] = mul2(make_float2(w.z, w.w), make_float2(a.w, b.w));
-            ws.p[2 * q] = mul2(make_float2(m.x, m.y), make_float2(a.x, b.x));
-            ws.p[2 * q + 1] = mul2(make_float2(m.z, m.w), make_float2(a.z, b.z));
+            const float2 c0 = mul2(make_float2(w.x, w.y), make_float2(a.y, b.y));
+            const float2 c1 = mul2(make_float2(w.z, w.w), make_float2(a.w, b.w));
+            const float2 s0 = mul2(make_float2(m.x, m.y), make_float2(a.x, b.x));
+            const float2 s1 = mul2(make_float2(m.z, m.w), make_float2(a.z, b.z));
+            factors[warp][q][lane] = make_float4(c0.x, c0.y, c1.x, c1.y);
+            factors[warp][4 + q][lane] = make_float4(s0.x, s0.y, s1.x, s1.y);
         }
         if (TEAM > 1) __syncthreads(); else __syncwarp();  // the next pass overwrites the table
         const Place at = place_of(mine, pass * TPW + tl);
         const bool live = at.page >= 0;
         uint8_t* block = p.cache + (live ? (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) : 0);
         const int row = at.slot % kQcBlock;
+        const int64_t t = min(t0 + pass * TPW + tl, p.T - 1);
+        const T* kp = static_cast<const T*>(p.k) + t * p.k_tok_stride + g0 * p.k_head_stride + e0;
+        const T* vp = static_cast<const T*>(p.v) + t * p.v_tok_stride + g0 * p.v_head_stride + e0;
         for (int g = g0; g < g1; g += TEAM) {
-            vr.load(vp);
+            Row16<T> kr, ko, vr;
+            ko.zero();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                kr.load8(c, kp + 16 * c);
+                if (mate[c]) ko.load8(c, kp + 16 * c + mate[c]);
+                vr.load8(c, vp + 16 * c);
+            }
+            kp += TEAM * p.k_head_stride;
             vp += TEAM * p.v_head_stride;
             Vec16 x, o;
             kr.get(x);
-            ko.get(o);
-            // the next K rows: the next head's, or the next pass's first
-            if (g + TEAM < g1) {
-                kp += TEAM * p.k_head_stride;
-                load_k();
-            } else if (pass + 1 < passes) {
-                start(pass + 1);
-                load_k();
-            }
             float2 s2 = mul2(x.p[0], x.p[0]);
 #pragma unroll
             for (int i = 1; i < 8; ++i) s2 = fma2(x.p[i], x.p[i], s2);
@@ -303,11 +292,17 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
 #pragma unroll
             for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
             const float2 rinv = both(inv_sqrt(ss / (float)D + p.eps));
+            ko.get(o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x.p[i] = mul2(fma2(x.p[i], wc.p[i], mul2(o.p[i], ws.p[i])), rinv);
-            encode_store(x, block, row, e0, D, live);
+            for (int q = 0; q < 4; ++q) {
+                const float4 wc = factors[warp][q][lane], ws = factors[warp][4 + q][lane];
+                x.p[2 * q] = mul2(fma2(x.p[2 * q], make_float2(wc.x, wc.y), mul2(o.p[2 * q], make_float2(ws.x, ws.y))), rinv);
+                x.p[2 * q + 1] =
+                    mul2(fma2(x.p[2 * q + 1], make_float2(wc.z, wc.w), mul2(o.p[2 * q + 1], make_float2(ws.z, ws.w))), rinv);
+            }
+            encode_store(x, block, row, lc, D, live);
             vr.get(x);
-            encode_store(x, block + plane, row, e0, D, live);
+            encode_store(x, block + plane, row, lc, D, live);
             block += TEAM * head;
         }
     }
@@ -345,31 +340,31 @@ __global__ void __launch_bounds__(32 * kWarps)
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t0 = (blockIdx.x * (kWarps / team) + warp / team) * TPW * passes;
-    const int e0 = 16 * (lane % LPR), g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
+    const int lc = lane % LPR, e0 = first_feature(lc), g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
     if (t0 >= p.T || g0 >= g1) return;
     Place mine;  // of token t0 + lane
     const bool ok = report(lane < passes * TPW ? place_cached(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
     const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
-    const int j = (e0 >> 4) & 1, upper = (e0 >> 5) & 1;
-    const uint32_t sel = upper ? 0x7632 : 0x5410;
+    const uint32_t sel = (lc & 2) ? 0x7632 : 0x5410;  // the group's half of a word
     for (int pass = 0; pass < passes; ++pass) {
         const Place at = place_of(mine, pass * TPW + lane / LPR);
         if (at.page < 0) continue;  // no lane of this token goes on; the shuffles above are whole again next time
         const int64_t t = t0 + pass * TPW + lane / LPR;
         const int row = at.slot % kQcBlock;
-        const uint8_t* src = p.cache + (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) +
-                             (e0 >> 6) * 512 + row * 32 + 16 * j;
-        const int par = 8 * D + ((e0 >> 5) * 16 + row) * 2 - ((e0 >> 6) * 512 + row * 32 + 16 * j);
+        const int codes = (lc >> 2) * 512 + row * 32 + 8 * (lc & 1);
+        const uint8_t* src = p.cache + (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) + codes;
+        const int par = 8 * D + ((lc >> 1) * 16 + row) * 2 - codes;
         T* kout = static_cast<T*>(p.k) + (t * p.G + g0) * D + e0;
         T* vout = static_cast<T*>(p.v) + (t * p.G + g0) * D + e0;
 #pragma unroll 4
         for (int g = g0; g < g1; g += team) {
-            uint4 w[2];
+            uint2 w[2][2];
             uint32_t s[2], c[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // K and V
-                w[i] = *reinterpret_cast<const uint4*>(src + i * plane);
+                w[i][0] = *reinterpret_cast<const uint2*>(src + i * plane);
+                w[i][1] = *reinterpret_cast<const uint2*>(src + i * plane + 16);
                 s[i] = *reinterpret_cast<const uint16_t*>(src + i * plane + par);
                 c[i] = *reinterpret_cast<const uint16_t*>(src + i * plane + par + D);
             }
@@ -377,8 +372,8 @@ __global__ void __launch_bounds__(32 * kWarps)
             for (int i = 0; i < 2; ++i) {
                 T* out = i ? vout : kout;
                 const uint32_t s2 = s[i] * 0x10001u, c2 = c[i] * 0x10001u;
-                decode8(__byte_perm(w[i].x, w[i].y, sel), s2, c2, out);
-                decode8(__byte_perm(w[i].z, w[i].w, sel), s2, c2, out + 8);
+                decode8(__byte_perm(w[i][0].x, w[i][0].y, sel), s2, c2, out);
+                decode8(__byte_perm(w[i][1].x, w[i][1].y, sel), s2, c2, out + 16);
             }
             src += team * head;
             kout += team * D;
