@@ -155,45 +155,72 @@ __device__ __forceinline__ bool report(int what, unsigned int* status) {
     return what == kLive;
 }
 
-// Quantise this lane's 16 features (two neighbouring lanes share a group of 32, four a
-// slab) and store them at row `row` of `block`.  All lanes of the warp.
-__device__ __forceinline__ void encode_store(const Vec16& x, uint8_t* block, int row, int lc, int d, bool live) {
-    float hi = max_nan(x.p[0].x, x.p[0].y), lo = min_nan(x.p[0].x, x.p[0].y);
+// Quantise this lane's features of K and of V (neighbouring lanes share a group of 32, four
+// a slab) and store them at row `row` of `block` and of the V plane's block.  The two go
+// together so that one's chain of extremes, scale and reciprocal fills the other's waits.
+// All lanes of the warp.
+__device__ __forceinline__ void encode_store(const Vec16 (&x)[2], uint8_t* block, int64_t plane, int row, int lc, int d,
+                                             bool live) {
+    float hi[2], lo[2];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        hi = max_nan(hi, x.p[i].x, x.p[i].y);
-        lo = min_nan(lo, x.p[i].x, x.p[i].y);
+    for (int n = 0; n < 2; ++n) {
+        hi[n] = max_nan(x[n].p[0].x, x[n].p[0].y);
+        lo[n] = min_nan(x[n].p[0].x, x[n].p[0].y);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            hi[n] = max_nan(hi[n], x[n].p[i].x, x[n].p[i].y);
+            lo[n] = min_nan(lo[n], x[n].p[i].x, x[n].p[i].y);
+        }
     }
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
-    const QcGroup q = qc_group(lo, hi);
-    uint32_t w[2];
-    const float2 ends = fma2(add2(make_float2(lo, hi), both(-q.centre)), both(q.inv), both(kQcMagic + 8.f));
-    if (__all_sync(0xffffffffu, ends.x >= kQcMagic && ends.y <= kQcMagic + 15.f)) {
-        w[0] = encode8<false>(x.p, q);
-        w[1] = encode8<false>(x.p + 4, q);
+    QcGroup q[2];
+    bool inside = true;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        hi[n] = max_nan(hi[n], __shfl_xor_sync(0xffffffffu, hi[n], 1));
+        lo[n] = min_nan(lo[n], __shfl_xor_sync(0xffffffffu, lo[n], 1));
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        q[n] = qc_group(lo[n], hi[n]);
+        const float2 ends = fma2(add2(make_float2(lo[n], hi[n]), both(-q[n].centre)), both(q[n].inv), both(kQcMagic + 8.f));
+        inside = inside && ends.x >= kQcMagic && ends.y <= kQcMagic + 15.f;
+    }
+    uint32_t w[2][2];
+    if (__all_sync(0xffffffffu, inside)) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            w[n][0] = encode8<false>(x[n].p, q[n]);
+            w[n][1] = encode8<false>(x[n].p + 4, q[n]);
+        }
     } else {
-        w[0] = encode8<true>(x.p, q);
-        w[1] = encode8<true>(x.p + 4, q);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            w[n][0] = encode8<true>(x[n].p, q[n]);
+            w[n][1] = encode8<true>(x[n].p + 4, q[n]);
+        }
     }
     // lanes j and j ^ 2 of a slab hold the same features of its two groups, which meet in the
     // words of both runs; the first group's lane stores the words of run 0, the other run 1's
     const int odd = lc & 1, upper = (lc >> 1) & 1;
-    const uint32_t o = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[1], 2);
-    if (!live) return;
-    const uint32_t a = upper ? o : w[0], b = upper ? w[1] : o;
-    *reinterpret_cast<uint2*>(block + (lc >> 2) * 512 + row * 32 + 16 * upper + 8 * odd) =
-        make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
-    // the group's two lanes store its scale and its centre
-    reinterpret_cast<uint16_t*>(block + 8 * d)[odd * (d / 2) + (lc >> 1) * 16 + row] =
-        (uint16_t)(odd ? q.bits >> 16 : q.bits);
+    const int at = (lc >> 2) * 512 + row * 32 + 16 * upper + 8 * odd;
+    const int par = 8 * d + (odd * (d / 2) + (lc >> 1) * 16 + row) * 2;  // the group's lanes: its scale, its centre
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, upper ? w[n][0] : w[n][1], 2);
+        const uint32_t a = upper ? o : w[n][0], b = upper ? w[n][1] : o;
+        if (live) {
+            uint8_t* to = block + n * plane;
+            *reinterpret_cast<uint2*>(to + at) = make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+            *reinterpret_cast<uint16_t*>(to + par) = (uint16_t)(odd ? q[n].bits >> 16 : q[n].bits);
+        }
+    }
 }
 
 // A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass.  `TEAM` of the block's
 // warps (one or all) take the same tokens, `passes` passes of them, and every TEAM-th of the
 // heads [blockIdx.y heads, ...); they make the sines and cosines together.
 template <int D, typename T, int TEAM>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 4)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 6 : 4)
     qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     // sines and cosines of a pass, {sin, cos} of frequencies 2u, 2u + 1 in element
@@ -283,11 +310,11 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 4)
             }
             kp += TEAM * p.k_head_stride;
             vp += TEAM * p.v_head_stride;
-            Vec16 x, o;
-            kr.get(x);
-            float2 s2 = mul2(x.p[0], x.p[0]);
+            Vec16 x[2], o;
+            kr.get(x[0]);
+            float2 s2 = mul2(x[0].p[0], x[0].p[0]);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) s2 = fma2(x.p[i], x.p[i], s2);
+            for (int i = 1; i < 8; ++i) s2 = fma2(x[0].p[i], x[0].p[i], s2);
             float ss = s2.x + s2.y;
 #pragma unroll
             for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
@@ -296,13 +323,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 4)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 wc = factors[warp][q][lane], ws = factors[warp][4 + q][lane];
-                x.p[2 * q] = mul2(fma2(x.p[2 * q], make_float2(wc.x, wc.y), mul2(o.p[2 * q], make_float2(ws.x, ws.y))), rinv);
-                x.p[2 * q + 1] =
-                    mul2(fma2(x.p[2 * q + 1], make_float2(wc.z, wc.w), mul2(o.p[2 * q + 1], make_float2(ws.z, ws.w))), rinv);
+                x[0].p[2 * q] = mul2(fma2(x[0].p[2 * q], make_float2(wc.x, wc.y), mul2(o.p[2 * q], make_float2(ws.x, ws.y))), rinv);
+                x[0].p[2 * q + 1] =
+                    mul2(fma2(x[0].p[2 * q + 1], make_float2(wc.z, wc.w), mul2(o.p[2 * q + 1], make_float2(ws.z, ws.w))), rinv);
             }
-            encode_store(x, block, row, lc, D, live);
-            vr.get(x);
-            encode_store(x, block + plane, row, lc, D, live);
+            vr.get(x[1]);
+            encode_store(x, block, plane, row, lc, D, live);
             block += TEAM * head;
         }
     }
@@ -385,16 +411,18 @@ __global__ void __launch_bounds__(32 * kWarps)
 // How a call is cut: passes a warp takes (their lookups go together), KV heads of a block,
 // warps that share a token's heads.  A call too small to fill the device with one warp for
 // all heads of its tokens takes one pass and spreads the heads, over a block's warps first.
+// (Passes of a long call: the write of 131072 tokens, 2 x 256, takes 106 us with two and 101
+// with four; the read of 211k tokens, 4 x 128, 107 with two and 119 with four.)
 struct Cut {
     int passes, heads, team;
     dim3 grid;
 };
 template <int D>
-Cut cut_of(int T, int G) {
+Cut cut_of(int T, int G, int passes) {
     constexpr int TPW = 32 / (D / 16);
     const int64_t want = 8 * (int64_t)device_sm_count(), groups = ((int64_t)T + TPW - 1) / TPW;
-    Cut c{2, G, 1, dim3()};
-    if (groups < 2 * want) c.passes = 1;
+    Cut c{passes, G, 1, dim3()};
+    if (groups < passes * want) c.passes = 1;
     if (G > 1 && groups < want) c.team = kWarps;
     while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < want) c.heads = (c.heads + 1) / 2;
     const int tokens = kWarps / c.team * TPW * c.passes;
@@ -404,7 +432,7 @@ Cut cut_of(int T, int G) {
 
 template <int D>
 cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G);
+    const Cut c = cut_of<D>(p.T, p.G, 4);
     auto kernel = fp32 ? (c.team > 1 ? qcache_write_kernel<D, float, kWarps> : qcache_write_kernel<D, float, 1>)
                        : (c.team > 1 ? qcache_write_kernel<D, bf16, kWarps> : qcache_write_kernel<D, bf16, 1>);
     kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
@@ -413,7 +441,7 @@ cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) 
 
 template <int D>
 cudaError_t read_d(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G);
+    const Cut c = cut_of<D>(p.T, p.G, 2);
     auto kernel = fp32 ? qcache_read_kernel<D, float> : qcache_read_kernel<D, bf16>;
     kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads, c.team);
     return cudaGetLastError();
