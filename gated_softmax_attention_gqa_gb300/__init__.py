@@ -355,63 +355,11 @@ def gattn_qcache_shape(num_pages, G, page_size, d):
     return (2, num_pages, G, page_size // 16, 10 * d)
 
 
-# A decode step is a few microseconds on the GPU, so these wrappers stay lean: device
-# indices instead of device objects, the raw handle of the current stream, no helper
-# objects per call.
+# The layout checks and the calls are in csrc/qcache_binding.cpp: a decode step is ten
+# microseconds on the GPU, and checks written here would set its pace.
 
-def _qcache_geometry(qcache, block_table):
-    """(num_pages, G, page_size, d, B, max_pages, device index) of a cache and its table, checked."""
-    if qcache.dim() != 5 or block_table.dim() != 2:
-        raise ValueError("qcache is [2,num_pages,G,page_size/16,10 d], block_table [B,max_pages]")
-    planes, num_pages, G, blocks, row = qcache.shape
-    if planes != 2 or row % 10 or qcache.dtype is not torch.uint8 or not qcache.is_contiguous():
-        raise ValueError("qcache must be a contiguous uint8 [2,num_pages,G,page_size/16,10 d] tensor")
-    dev = qcache.get_device()
-    if block_table.dtype is not torch.int32 or not block_table.is_contiguous() or block_table.get_device() != dev:
-        raise ValueError("block_table must be a contiguous int32 [B,max_pages] tensor on the cache's device")
-    B, max_pages = block_table.shape
-    return num_pages, G, 16 * blocks, row // 10, B, max_pages, dev
-
-
-def _qcache_index(name, t, n, dev):
-    if t.shape != (n,) or t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} on the cache's device")
-    return t.data_ptr()
-
-
-def _qcache_dense(name, t, shape, dtype, dev):
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on the cache's device")
-    return t.data_ptr()
-
-
-def _qcache_stride(size, stride, name):
-    """A dimension's stride for the C call, where 0 selects the contiguous default: a
-    dimension of one has no stride to speak of, and a broadcast one cannot be passed."""
-    if size <= 1:
-        return 0
-    if stride == 0:
-        raise ValueError(f"{name}: broadcast (stride 0) views are not supported; pass a contiguous copy")
-    return stride
-
-
-def _qcache_call(dev, stream, fn, *args):
-    """fn(*args, stream handle) with device `dev` current."""
-    if dev < 0:
-        raise ValueError("the tensors must be on a CUDA device")
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch._C._cuda_getDevice():
-        return fn(*args, s)
-    with torch.cuda.device(dev):
-        return fn(*args, s)
-
-
-def _empty_on(stream, shape, dtype, device):
-    """torch.empty whose memory belongs to the stream that will use it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _qcache_stream(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def gattn_qcache_write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens=None, *, rotary_dim, rope_base, eps=1e-6,
@@ -425,25 +373,8 @@ def gattn_qcache_write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens=N
     length of 0 marks an unused row.
     seqlens [B] int32 on the device: tokens in each sequence after the write.
     block_table [B,max_pages] int32: the page of each page_size-token stretch."""
-    num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
-    dtype = k.dtype
-    if k.dim() != 3 or k.shape != v.shape or k.shape != (k.shape[0], G, d):
-        raise ValueError(f"k and v must both be [T,{G},{d}], as the cache's heads")
-    T = k.shape[0]
-    (kt, kh, ke), (vt, vh, ve) = k.stride(), v.stride()
-    if ke != 1 or ve != 1:
-        raise ValueError("k and v: the last dimension must be contiguous")
-    if dtype not in DTYPES or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev:
-        raise ValueError("k and v must both be bfloat16 or both be float32, on the cache's device")
-    if cu_seqlens is None and T != B:
-        raise ValueError(f"without cu_seqlens every sequence gets one token: {T} tokens, {B} sequences")
-    st = _qcache_call(
-        dev, stream, _lib.load().gattn_qcache_write, k.data_ptr(), v.data_ptr(), qcache.data_ptr(),
-        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, dev),
-        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, dev),
-        _qcache_dense("knorm_w", knorm_w, (d,), dtype, dev), T, B, G, d, rotary_dim, rope_base, eps,
-        _qcache_stride(T, kt, "k"), _qcache_stride(G, kh, "k"), _qcache_stride(T, vt, "v"), _qcache_stride(G, vh, "v"),
-        DTYPES[dtype])
+    st = _lib.qcache().write(k, v, qcache, block_table, seqlens, knorm_w, cu_seqlens, rotary_dim, rope_base, eps,
+                             _qcache_stream(stream))
     if st:
         check(st, "gattn_qcache_write")
     return qcache
@@ -458,34 +389,13 @@ def gattn_qcache_read(qcache, block_table, starts=None, cu_seqlens=None, *, tota
     sequence b; both are int32 on the device.  cu_seqlens None: one token per sequence
     (total = B); starts None: from token 0.  total is the number of rows, cu_seqlens[B] or
     more (rows past it are left as they were).  k_out, v_out: contiguous tensors to fill."""
-    num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
-    if total is None:
-        if cu_seqlens is not None and k_out is None:
-            raise ValueError("total (the number of rows) is needed with cu_seqlens")
-        total = B if cu_seqlens is None else k_out.shape[0]
-    if cu_seqlens is None and total != B:
-        raise ValueError("without cu_seqlens one token of each sequence is read")
-    if k_out is not None and v_out is not None:
-        dtype = k_out.dtype
-    elif k_out is not None or v_out is not None:
-        raise ValueError("k_out and v_out go together")
     if dtype not in DTYPES:
-        raise ValueError("the values are returned in bfloat16 or float32")
-    if k_out is None:
-        k_out = _empty_on(stream, (total, G, d), dtype, qcache.device)
-        v_out = _empty_on(stream, (total, G, d), dtype, qcache.device)
-        kp, vp = k_out.data_ptr(), v_out.data_ptr()
-    else:
-        kp = _qcache_dense("k_out", k_out, (total, G, d), dtype, dev)
-        vp = _qcache_dense("v_out", v_out, (total, G, d), dtype, dev)
-    st = _qcache_call(
-        dev, stream, _lib.load().gattn_qcache_read, qcache.data_ptr(), block_table.data_ptr(), num_pages, page_size,
-        max_pages, None if starts is None else _qcache_index("starts", starts, B, dev),
-        None if cu_seqlens is None else _qcache_index("cu_seqlens", cu_seqlens, B + 1, dev), total, B, G, d,
-        DTYPES[dtype], kp, vp)
+        raise ValueError("dtype must be bfloat16 or float32")
+    st, k, v = _lib.qcache().read(qcache, block_table, starts, cu_seqlens, total, DTYPES[dtype], k_out, v_out,
+                                  _qcache_stream(stream))
     if st:
         check(st, "gattn_qcache_read")
-    return k_out, v_out
+    return k, v
 
 
 def gattn_decode_qcache_workspace_size(B, H, G, d, Lmax) -> int:
@@ -502,47 +412,8 @@ def gattn_decode_qcache(q_new, qcache, block_table, seqlens, gate, qnorm_w, *, r
     [B,G,d] and knorm_w the new token is first written into the cache.  The rest as
     gattn_decode_paged.  Returns out [B,H*d]."""
     mode = _mode(gate_mode, gate_act, gate_additive)
-    num_pages, G, page_size, d, B, max_pages, dev = _qcache_geometry(qcache, block_table)
-    if q_new.dim() != 3 or q_new.dtype is not torch.bfloat16 or q_new.get_device() != dev:
-        raise ValueError("q_new must be a bfloat16 [B,H,d] tensor on the cache's device")
-    qb, H, qd = q_new.shape
-    qs, qh, qe = q_new.stride()
-    if qb != B or qd != d or qe != 1:
-        raise ValueError(f"q_new must be [{B},H,{d}], as the table and the cache, its last dimension contiguous")
-    layout = mode & 0x0F
-    gp, gs, gh = None, 0, 0
-    if layout:
-        want = (B, H, d) if layout == 1 else (B, H) if layout == 2 else (B, d)
-        if gate is None or gate.shape != want or gate.dtype is not torch.bfloat16 or gate.get_device() != dev:
-            raise ValueError(f"gate must be a bfloat16 {list(want)} tensor on the cache's device")
-        if layout != 2 and gate.stride(-1) != 1:
-            raise ValueError("gate: the last dimension must be contiguous")
-        gp, gs = gate.data_ptr(), _qcache_stride(B, gate.stride(0), "gate")
-        if layout != 3:
-            gh = _qcache_stride(H, gate.stride(1), "gate")
-    kp = vp = wp = None
-    if k_new is not None or v_new is not None or knorm_w is not None:
-        if k_new is None or v_new is None or knorm_w is None:
-            raise ValueError("an append needs k_new, v_new and knorm_w")
-        kp = _qcache_dense("k_new", k_new, (B, G, d), torch.bfloat16, dev)
-        vp = _qcache_dense("v_new", v_new, (B, G, d), torch.bfloat16, dev)
-        wp = _qcache_dense("knorm_w", knorm_w, (d,), torch.bfloat16, dev)
-    if out is None:
-        out = _empty_on(stream, (B, H * d), torch.bfloat16, qcache.device)
-        op = out.data_ptr()
-    else:
-        op = _qcache_dense("out", out, (B, H * d), torch.bfloat16, dev)
-    if workspace is None:
-        with torch.cuda.device(qcache.device):
-            need = gattn_decode_qcache_workspace_size(B, H, G, d, max_pages * page_size)
-        workspace = _empty_on(stream, (max(need, 1),), torch.uint8, qcache.device)
-    elif not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError("workspace must be a contiguous tensor on the cache's device")
-    st = _qcache_call(
-        dev, stream, _lib.load().gattn_decode_qcache, q_new.data_ptr(), kp, vp, qcache.data_ptr(),
-        block_table.data_ptr(), num_pages, page_size, max_pages, _qcache_index("seqlens", seqlens, B, dev), gp,
-        _qcache_dense("qnorm_w", qnorm_w, (d,), torch.bfloat16, dev), wp, B, H, G, d, rotary_dim, rope_base, eps, mode,
-        _qcache_stride(B, qs, "q_new"), _qcache_stride(H, qh, "q_new"), gs, gh, workspace.data_ptr(), workspace.nbytes, op)
+    st, out = _lib.qcache().decode(q_new, k_new, v_new, qcache, block_table, seqlens, gate, qnorm_w, knorm_w, rotary_dim,
+                                   rope_base, eps, mode, workspace, out, _qcache_stream(stream))
     if st:
         check(st, "gattn_decode_qcache")
     return out

@@ -29,6 +29,7 @@ EXPORTS = (
 )
 
 _lib = None
+_qcache = None
 
 _vp, _i, _i64, _sz, _d, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_double, ctypes.c_float
 
@@ -94,6 +95,20 @@ def load():
     lib.gattn_set_profile_events.argtypes = [_vp, _vp]
     _lib = lib
     return lib
+
+
+def qcache():
+    """The CPython module of the 4-bit cache's entry points; raises if it has not been built."""
+    global _qcache
+    if _qcache is None:
+        load()  # says how to build
+        try:
+            from . import _qcache as module
+        except ImportError as e:
+            raise RuntimeError(
+                "_qcache.so is not built for this torch; run `python -c \"import __graft_entry__ as g; g.build()\"`") from e
+        _qcache = module
+    return _qcache
 
 
 def strerror(status: int) -> str:

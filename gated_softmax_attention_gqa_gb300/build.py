@@ -3,12 +3,15 @@
 Each .cu file compiles in parallel with nvcc, then one shared library is linked
 with the CUDA runtime statically, so loading it needs no GPU and no libcudart
 of a particular version.  Set GATTN_PTXAS_VERBOSE=1 to print register and
-shared-memory usage per kernel.
+shared-memory usage per kernel.  Beside it the CPython module _qcache.so (the
+4-bit cache's tensor checks and calls) compiles with g++ against the installed
+torch and links to the library.
 """
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libgattn.so")
 SOURCES = ["api.cu", "prologue.cu", "prefill_tc.cu", "prefill_pair.cu", "prefill_fp32.cu", "decode.cu", "decode_noalloc.cu",
            "oproj.cu", "qcache.cu", "decode_qcache.cu", "qcache_api.cu"]
+BINDING = "qcache_binding.cpp"
+MODULE = os.path.join(HERE, "_qcache.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,10 +40,26 @@ def _flags():
     return f
 
 
+def _binding_compile(obj):
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], INCLUDE,
+            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(CSRC, BINDING), "-o", obj] + [
+        f"-I{d}" for d in dirs]
+
+
+def _binding_link(obj, to):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", to, obj, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "gattn.h"), __file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -53,6 +74,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         cmd = [exe] + _flags() + ["-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    binding = os.path.join(BUILD, BINDING.replace(".cpp", ".o"))
+    procs.append((BINDING, binding, subprocess.Popen(_binding_compile(binding), stdout=subprocess.PIPE,
+                                                     stderr=subprocess.STDOUT, text=True)))
     objs, failed = [], []
     for src, obj, p in procs:
         out, _ = p.communicate()
@@ -62,10 +86,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             failed.append(src)
         objs.append(obj)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("the compiler failed for: " + ", ".join(failed))
+    objs.remove(binding)
     tmp = LIB + ".tmp%d" % os.getpid()
-    subprocess.run([exe] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs, check=True)
+    subprocess.run([exe] + ARCH + ["-shared", "-cudart", "static", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o",
+                    tmp] + objs, check=True)
     os.replace(tmp, LIB)
+    tmp = MODULE + ".tmp%d" % os.getpid()
+    subprocess.run(_binding_link(binding, tmp), check=True)
+    os.replace(tmp, MODULE)
     return LIB
 
 
