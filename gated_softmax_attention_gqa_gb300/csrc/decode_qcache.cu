@@ -24,10 +24,15 @@
 //             into the next product's operand by a register transpose (movmatrix).
 //         O^T += V^T P^T   m16n8k16, bf16.  The rows are features, so the pairs an operand
 //             register holds are two keys of one feature: two words of neighbouring keys
-//             are interleaved once by halves, and every nibble position of the result is
-//             such a pair.  Code - 8 is exact in bf16; the scales multiply P instead
-//             (they are per key and group), and the centres' part, sum_k p_k centre_k, is
-//             one product for all groups.
+//             are interleaved by bytes.  A bf16 below 2^-125 counts in steps of 2^-133, so a
+//             byte's nibbles, masked, are bf16 numbers as they stand, and one multiply-add by
+//             2^127 makes them (code - 8) / 64 and (code - 8) / 4, exact; the output's
+//             rows are multiplied up at the end.  (With nibbles shifted down one by one and
+//             or-ed into 128, the shifts held the ALU: 64 sequences of 16k-32k tokens, d = 256,
+//             took 181 us, now 173; 4 of 60k-131k, d = 128, 55 us, now 53.)  The scales
+//             multiply P instead (they are per key and group), and the centres' part,
+//             sum_k p_k centre_k, is one product for all groups, in whose spare rows ones
+//             sum the weights.
 //   qdecode_combine_kernel  merges the partial states of pieces that several CTAs share
 //       and applies the gate; a (sequence, KV head) that one CTA covered is finished by
 //       that CTA.
@@ -118,6 +123,7 @@ struct WorkSplit {
 template <int D>
 __device__ void scan_batch(const int32_t* seqlens, int B, int Lmax, const Sequences& q, int* red) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) q.tiles[0] = q.live[0] = 0;
     int tiles0 = 0, live0 = 0;
     for (int first = 0; first < B; first += THREADS) {
         const int i = first + tid, L = i < B ? seqlens[i] : 0;
@@ -149,8 +155,6 @@ __device__ void scan_batch(const int32_t* seqlens, int B, int Lmax, const Sequen
         live0 = l;
         __syncthreads();
     }
-    if (tid == 0) q.tiles[0] = q.live[0] = 0;
-    __syncthreads();
 }
 
 // How many tiles lie ahead of unit u.
@@ -227,9 +231,9 @@ template <typename T>
 __device__ __forceinline__ T ld(const uint8_t* p) {
     return *reinterpret_cast<const T*>(p);
 }
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
-    asm("sub.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -243,21 +247,21 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
 
-// The gate applied to one output value (e: feature), and to four neighbouring ones.
+// The gate's logit for feature e of head h, and its application to an output value.
+__device__ __forceinline__ float gate_logit(const QcacheDecodeParams& p, int b, int h, int e) {
+    const int layout = gate_layout(p.gate_mode);
+    if (layout == GATTN_GATE_NONE) return 0.f;
+    const bf16* gp = static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride;
+    return __bfloat162float(layout == GATTN_GATE_ELEMENTWISE ? gp[h * p.gate_head_stride + e]
+                            : layout == GATTN_GATE_HEADWISE  ? gp[h * p.gate_head_stride]
+                                                             : gp[e]);
+}
 __device__ __forceinline__ float gate_apply(int mode, float z, float o) {
+    if (gate_layout(mode) == GATTN_GATE_NONE) return o;
     const float a = gate_act(z, sigmoidf_dev(z), mode);
     return gate_additive(mode) ? o + a : o * a;
 }
-__device__ __forceinline__ float gated(const QcacheDecodeParams& p, int b, int h, int e, float o) {
-    const int layout = gate_layout(p.gate_mode);
-    if (layout == GATTN_GATE_NONE) return o;
-    const bf16* gp = static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride;
-    return gate_apply(p.gate_mode,
-                      __bfloat162float(layout == GATTN_GATE_ELEMENTWISE ? gp[h * p.gate_head_stride + e]
-                                       : layout == GATTN_GATE_HEADWISE  ? gp[h * p.gate_head_stride]
-                                                                        : gp[e]),
-                      o);
-}
+// Four neighbouring output values.
 __device__ __forceinline__ void gated4(const QcacheDecodeParams& p, int b, int h, int e, float (&o)[4]) {
     const int layout = gate_layout(p.gate_mode);
     if (layout == GATTN_GATE_NONE) return;
@@ -269,24 +273,45 @@ __device__ __forceinline__ void gated4(const QcacheDecodeParams& p, int b, int h
     for (int k = 0; k < 4; ++k) o[k] = gate_apply(p.gate_mode, __bfloat162float(gp[k * step]), o[k]);
 }
 
+template <int D>
+struct QueryLanes {
+    static constexpr int LPH = D / 8, HPW = 32 / LPH;  // lanes per head, heads per warp and pass
+};
+// Brings the gate logits of heads h0 .. h0 + r - 1 into L2, a line of 64 a lane.
+template <int D>
+__device__ __forceinline__ void prefetch_gate(const QcacheDecodeParams& p, int b, int h0, int r, int lane) {
+    const int layout = gate_layout(p.gate_mode);
+    if (layout == GATTN_GATE_NONE) return;
+    const int lines = layout == GATTN_GATE_HEADWISE ? 1 : D / 64, h = layout == GATTN_GATE_HEAD_SHARED ? 0 : h0 + lane / lines;
+    if (lane < (layout == GATTN_GATE_HEAD_SHARED ? 1 : r) * lines)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const bf16*>(p.gate) + b * p.gate_seq_stride +
+                                                      h * p.gate_head_stride + lane % lines * 64));
+}
+
+// This lane's eight features of query head h of a KV head (head 0's for one past the last).
+template <int D>
+__device__ __forceinline__ uint4 load_query(const QcacheDecodeParams& p, int b, int g, int h) {
+    const int r = p.H / p.G;
+    return *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.q) + b * p.q_seq_stride +
+                                           (int64_t)(g * r + (h < r ? h : 0)) * p.q_head_stride +
+                                           8 * (threadIdx.x % QueryLanes<D>::LPH));
+}
+template <int D>
+__device__ __forceinline__ uint4 load_first_query(const QcacheDecodeParams& p, int b, int g) {
+    return load_query<D>(p, b, g, (int)threadIdx.x / QueryLanes<D>::LPH);
+}
 // The queries of one piece as B fragments (all threads).  A thread takes eight
 // neighbouring features of a head; q' is scaled by a power of two that brings the
 // head's largest |q'| into [0.5, 1), so any norm weights fit fp16, and the power goes
 // into the logit scale.  Two of the four operand registers of a group hold q / 16
 // (the codes they meet sit one nibble higher).
 template <int D>
-__device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos, uint8_t* tail) {
+__device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos, uint4 qraw, uint4 wraw, uint8_t* tail) {
     using C = QdCfg<D>;
-    constexpr int LPH = D / 8, HPW = 32 / LPH;  // lanes per head, heads per warp and pass
+    constexpr int LPH = QueryLanes<D>::LPH, HPW = QueryLanes<D>::HPW;
     const int r = p.H / p.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     float2* table = reinterpret_cast<float2*>(tail + C::OFF_OBUF);
-    const int u = lane % LPH, e0 = 8 * u, hw = warp * HPW + lane / LPH;
-    auto load_q = [&](int h) {
-        return *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.q) + b * p.q_seq_stride +
-                                               (int64_t)(g * r + (h < r ? h : 0)) * p.q_head_stride + e0);
-    };
-    const uint4 wraw = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(p.qnorm_w) + e0);
-    uint4 qraw = load_q(hw);
+    const int u = lane % LPH, e0 = 8 * u;
     __syncthreads();  // the previous piece has left the fragments and the merge buffer
     for (int i = tid; i < (p.rd >> 1); i += THREADS) {
         float s, c;
@@ -301,7 +326,7 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
         float x[8], w[8], ss = 0.f;
         unpack8(qraw, x);
         unpack8(wraw, w);
-        if (h0 + NW * HPW < r) qraw = load_q(h + NW * HPW);
+        if (h0 + NW * HPW < r) qraw = load_query<D>(p, b, g, h + NW * HPW);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             ss = fmaf(x[i], x[i], ss);
@@ -402,14 +427,23 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     int sent = 0;
     uint64_t src[C::NB] = {};
     TileAt at = {};  // first the CTA's first tile, then the piece at hand
+    uint4 qraw = {}, wraw = {};  // its queries and their norm weights as loaded
+    auto load_queries = [&]() {
+        qraw = load_first_query<D>(p, at.b, at.g);
+        wraw = reinterpret_cast<const uint4*>(p.qnorm_w)[threadIdx.x % QueryLanes<D>::LPH];
+        if (warp == 0) prefetch_gate<D>(p, at.b, at.g * r, r, lane);
+    };
     auto send = [&](int stage) {  // all lanes; tile x0 + sent into `stage`
         if (sent >= n_tiles) return;
         if ((sent & 31) == 0) {
 #pragma unroll
             for (int j = 0; j < C::NB; ++j) src[j] = 0;
             const TileAt t = tile_at(x0 + min(sent + lane, n_tiles - 1), seqs, p.B, p.G);
-            if (sent == 0) at = TileAt{__shfl_sync(0xffffffffu, t.b, 0), __shfl_sync(0xffffffffu, t.g, 0),
-                                       __shfl_sync(0xffffffffu, t.i, 0), __shfl_sync(0xffffffffu, t.nt, 0)};
+            if (sent == 0) {
+                at = TileAt{__shfl_sync(0xffffffffu, t.b, 0), __shfl_sync(0xffffffffu, t.g, 0),
+                            __shfl_sync(0xffffffffu, t.i, 0), __shfl_sync(0xffffffffu, t.nt, 0)};
+                load_queries();  // ahead of the copies, behind which they would wait 2 us
+            }
             if (sent + lane < n_tiles) {
 #pragma unroll
                 for (int j = 0; j < C::NB; ++j) {
@@ -466,9 +500,9 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     // V words are read so that the four lanes of a quad touch different banks: the upper
     // two take the pair's second key first, and the interleave undoes it
     const int kf = 2 * t + (t >> 1), ks = 2 * t + 1 - (t >> 1);
-    const uint32_t sel_lo = t < 2 ? 0x5410u : 0x1054u, sel_hi = t < 2 ? 0x7632u : 0x3276u;
-    const uint32_t one_f16 = opaque(0x64006400u), one_bf16 = opaque(0x43004300u);  // 1024, 128
-    constexpr uint32_t kMid = 0x43084308u;                                         // 136
+    const uint32_t sel_lo = t < 2 ? 0x0400u : 0x0004u, sel_hi = t < 2 ? 0x0602u : 0x0206u;  // bytes 0 and 2
+    const uint32_t one_f16 = opaque(0x64006400u);  // 1024
+    constexpr uint32_t kUp = 0x7F007F00u, kMid64 = 0xBE00BE00u, kMid4 = 0xC000C000u;  // 2^127, -1/8, -2
     int st = 0, done = 0;  // stage and number of the unit at hand
     uint32_t phase = 0;
     bool dead = false;
@@ -492,7 +526,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         const int L = seqs.lens[at.b];
         n += i1 - i0;
         const bool alone = i0 == 0 && i1 == at.nt;
-        make_queries<D>(p, at.b, at.g, L - 1, tail);
+        make_queries<D>(p, at.b, at.g, L - 1, qraw, wraw, tail);
         const float2 qsc = ld<float2>(tail + C::OFF_QSC + t * 8);
         const uint32_t qhi = ld<uint32_t>(tail + C::OFF_QSUM + gid * 16 + t * 4);
         const uint32_t qlo = ld<uint32_t>(tail + C::OFF_QSUM + 128 + gid * 16 + t * 4);
@@ -501,9 +535,9 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         float oacc[2 * C::NG][4], cacc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int m = 0; m < 2 * C::NG; ++m) oacc[m][0] = oacc[m][1] = oacc[m][2] = oacc[m][3] = 0.f;
-        // softmax state of heads 2t and 2t + 1: the reference is the same in every lane that
-        // holds the head, the sum is over this lane's keys
-        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        // the softmax reference of heads 2t and 2t + 1, the same in every lane that holds the
+        // head; the sums of the weights, as they are used, are cacc[2] and cacc[3]
+        float m_run[2] = {-INFINITY, -INFINITY};
 
         for (int i = i0; i < i1; ++i) {
             const int key0 = (i * NW + warp) * C::NB * kQcBlock;
@@ -551,11 +585,12 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                         const int grp = 2 * sl + hf;
                         const uint4 qf = ld<uint4>(qfp + grp * 512);
                         const float4 ci = ld<float4>(cip + grp * 64);
-                        const uint32_t sel = hf ? 0x7632 : 0x5410;
+                        const uint32_t sel = hf ? 0x0602 : 0x0400;  // bytes 0 and 2 of the pair of halves
 #pragma unroll
                         for (int n2 = 0; n2 < NB; ++n2) {
                             const uint32_t c0 = __byte_perm(wa[n2].x, wa[n2].y, sel), c1 = __byte_perm(wb[n2].x, wb[n2].y, sel);
-                            const uint32_t d0 = c0 >> 8, d1 = c1 >> 8;
+                            const uint32_t d0 = __byte_perm(wa[n2].x, wa[n2].y, sel + 0x0101);
+                            const uint32_t d1 = __byte_perm(wb[n2].x, wb[n2].y, sel + 0x0101);
                             float a[4];
                             mma_f16_16816(a, and_or<0x000F000Fu>(c0, one_f16), and_or<0x000F000Fu>(c1, one_f16),
                                           and_or<0x00F000F0u>(c0, one_f16), and_or<0x00F000F0u>(c1, one_f16), qf.x, qf.y,
@@ -601,8 +636,6 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     const float a1 = t1 == m_run[1] ? 1.f : ex2_approx(m_run[1] - t1);
                     m_run[0] = t0;
                     m_run[1] = t1;
-                    l_run[0] *= a0;
-                    l_run[1] *= a1;
 #pragma unroll
                     for (int m = 0; m < 2 * C::NG; ++m) {
                         oacc[m][0] *= a0;
@@ -612,6 +645,8 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     }
                     cacc[0] *= a0;
                     cacc[1] *= a1;
+                    cacc[2] *= a0;
+                    cacc[3] *= a1;
                 }
                 uint32_t pr[NB][2];
 #pragma unroll
@@ -620,11 +655,9 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     for (int k = 0; k < 2; ++k) {
                         const uint32_t w =
                             pack_bf16x2(ex2_approx(s[n2][2 * k] - m_run[0]), ex2_approx(s[n2][2 * k + 1] - m_run[1]));
-                        l_run[0] += bf16_lo(w);  // the sum of the weights as they are used
-                        l_run[1] += bf16_hi(w);
                         pr[n2][k] = transpose8x8(w);  // head gid, keys 8k + 2t, 8k + 2t + 1
                     }
-                // ---- centres: row g of A is group g
+                // ---- centres: row g of A is group g; rows 8 and on are ones and sum the weights
 #pragma unroll
                 for (int n2 = 0; n2 < NB; ++n2) {
                     const uint8_t* ca = vb + n2 * BB + 9 * D + gid * 32 + t * 4;
@@ -633,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                         a0 = ld<uint32_t>(ca);
                         a2 = ld<uint32_t>(ca + 16);
                     }
-                    mma_bf16_16816(cacc, a0, 0u, a2, 0u, pr[n2][0], pr[n2][1]);
+                    mma_bf16_16816(cacc, a0, 0x3F803F80u, a2, 0x3F803F80u, pr[n2][0], pr[n2][1]);
                 }
                 // ---- O^T += V^T P^T
                 const uint8_t* vf = vb + gid * 4 + kf * 32;
@@ -650,20 +683,19 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                         for (int hf = 0; hf < 2; ++hf) {
                             const int grp = 2 * sl + hf;
                             const uint32_t sel = hf ? sel_hi : sel_lo;
-                            const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
+                            const uint32_t w0[2] = {__byte_perm(f0, s0, sel), __byte_perm(f0, s0, sel + 0x0101u)};
+                            const uint32_t w1[2] = {__byte_perm(f1, s1, sel), __byte_perm(f1, s1, sel + 0x0101u)};
                             const uint8_t* vpn = vp + n2 * BB + grp * 32;
                             const uint32_t p0 = mul_bf16x2(pr[n2][0], ld<uint32_t>(vpn));
                             const uint32_t p1 = mul_bf16x2(pr[n2][1], ld<uint32_t>(vpn + 16));
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                uint32_t a[4];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const int sh = 4 * (2 * m + k);
-                                    a[k] = sub_bf16x2(and_or<0x000F000Fu>(w0 >> sh, one_bf16), kMid);
-                                    a[2 + k] = sub_bf16x2(and_or<0x000F000Fu>(w1 >> sh, one_bf16), kMid);
-                                }
-                                mma_bf16_16816(oacc[2 * grp + m], a[0], a[1], a[2], a[3], p0, p1);
+                                // (code - 8) / 64 in rows 0-7, (code - 8) / 4 in rows 8-15
+                                const uint32_t a0 = fma_bf16x2(w0[m] & 0x000F000Fu, kUp, kMid64);
+                                const uint32_t a1 = fma_bf16x2(w0[m] & 0x00F000F0u, kUp, kMid4);
+                                const uint32_t a2 = fma_bf16x2(w1[m] & 0x000F000Fu, kUp, kMid64);
+                                const uint32_t a3 = fma_bf16x2(w1[m] & 0x00F000F0u, kUp, kMid4);
+                                mma_bf16_16816(oacc[2 * grp + m], a0, a1, a2, a3, p0, p1);
                             }
                         }
                     }
@@ -675,12 +707,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         // -------- end of the piece: merge the four warps, then finish or hand over
         float* ml = reinterpret_cast<float*>(tail + C::OFF_ML);
         float* obuf = reinterpret_cast<float*>(tail + C::OFF_OBUF);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], o);
-            l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], o);
-        }
-        if (gid == 0) reinterpret_cast<float4*>(ml)[warp * 4 + t] = make_float4(m_run[0], l_run[0], m_run[1], l_run[1]);
+        if (gid == 0) reinterpret_cast<float4*>(ml)[warp * 4 + t] = make_float4(m_run[0], cacc[2], m_run[1], cacc[3]);
         __syncthreads();
         // weight of this warp's state for the lane's two heads
         float f[2];
@@ -703,27 +730,35 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
             }
             reinterpret_cast<float2*>(tail + C::OFF_TOT)[threadIdx.x] = make_float2(mx, l);
         }
-        // four rounds; in each the warps add to different quarters of the features
+        // four rounds; in each the warps add to different quarters of the features, loads first
         constexpr int MQ = C::NG / 2;  // row tiles a quarter
 #pragma unroll 1
         for (int k = 0; k < NW; ++k) {
             const int quarter = (warp + k) & 3;
 #pragma unroll
-            for (int m = 0; m < 2 * C::NG; ++m) {
-                if (m / MQ != quarter) continue;
-                const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * (m >> 1) + t);
-                const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * (m >> 1) + t);
+            for (int qt = 0; qt < 4; ++qt) {
+                if (qt != quarter) continue;
+                float2 o[MQ][2];
+                auto place = [&](int m, int e) {
+                    return reinterpret_cast<float2*>(obuf + (2 * t + e) * C::OROW + (m >> 1) * 32 + gid * 4 + (m & 1) * 2);
+                };
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int h = 2 * t + e;
-                    float2* at2 = reinterpret_cast<float2*>(obuf + h * C::OROW + (m >> 1) * 32 + gid * 4 + (m & 1) * 2);
-                    if (h < r) {
-                        float2 o = k ? *at2 : make_float2(0.f, 0.f);
+                for (int i = 0; i < MQ; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        o[i][e] = k && 2 * t + e < r ? *place(qt * MQ + i, e) : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < MQ; ++i) {
+                    const int m = qt * MQ + i;
+                    const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * (m >> 1) + t);
+                    const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * (m >> 1) + t);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
                         if (f[e] != 0.f) {
-                            o.x = fmaf(f[e], oacc[m][e] + (e ? c1 : c0), o.x);
-                            o.y = fmaf(f[e], oacc[m][2 + e] + (e ? c1 : c0), o.y);
+                            o[i][e].x = fmaf(f[e], fmaf(64.f, oacc[m][e], e ? c1 : c0), o[i][e].x);
+                            o[i][e].y = fmaf(f[e], fmaf(4.f, oacc[m][2 + e], e ? c1 : c0), o[i][e].y);
                         }
-                        *at2 = o;
+                        if (2 * t + e < r) *place(m, e) = o[i][e];
                     }
                 }
             }
@@ -757,6 +792,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
             if (at.b == p.B) break;
             at.nt = seqs.tiles[at.b + 1] - seqs.tiles[at.b];
         }
+        load_queries();
     }
     // every copy that was sent lands before the block leaves (none is left unless a wait ran out)
     for (; done < sent; ++done) mbar_wait_drain(bars + 8 * (done % n_stages), (uint32_t)(done / n_stages) & 1u, p.status);
@@ -767,7 +803,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 // the warps meet in shared memory.  A sequence of length 0 gets the gate of an empty sum.
 template <int D, int NWC>
 __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_constant__ QcacheDecodeParams p, int n_ctas) {
-    constexpr int DPL = D / 32, CH = 4;
+    constexpr int DPL = D / 32, CH = NWC == 8 ? 8 : 4, EPT = (D + 32 * NWC - 1) / (32 * NWC);
     __shared__ float sm[NWC][2], so[NWC][D];
     __shared__ int units[NWC][2];
     const int b = blockIdx.x / p.H, hq = blockIdx.x % p.H;
@@ -794,6 +830,12 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
         total += units[w][1];
     }
     bf16* out = static_cast<bf16*>(p.out) + ((int64_t)b * p.H + hq) * D;
+    float z[EPT];  // the gate of features threadIdx.x + k 32 NWC
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+        const int e = threadIdx.x + k * 32 * NWC;
+        z[k] = e < D ? gate_logit(p, b, hq, e) : 0.f;
+    }
     int n_slots = 0, c0 = 0;
     if (nt) {
         const WorkSplit split(p.G * total, n_ctas);
@@ -809,7 +851,10 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
     pdl_wait_prerequisites();
     if (nt == 0) {
         if (L == 0) {
-            for (int e = threadIdx.x; e < D; e += 32 * NWC) out[e] = __float2bfloat16_rn(gated(p, b, hq, e, 0.f));
+#pragma unroll
+            for (int k = 0; k < EPT; ++k)
+                if (threadIdx.x + k * 32 * NWC < D)
+                    out[threadIdx.x + k * 32 * NWC] = __float2bfloat16_rn(gate_apply(p.gate_mode, z[k], 0.f));
         } else if (threadIdx.x == 0 && hq == 0) {
             atomicOr(p.status, GATTN_DEVICE_BAD_SEQLEN);
         }
@@ -863,11 +908,14 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
         f[w] = sm[w][0] == -INFINITY ? 0.f : ex2_approx(sm[w][0] - mx);
         l += f[w] != 0.f ? f[w] * sm[w][1] : 0.f;
     }
-    for (int e = threadIdx.x; e < D; e += 32 * NWC) {
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+        const int e = threadIdx.x + k * 32 * NWC;
+        if (e >= D) break;
         float o = 0.f;
 #pragma unroll
         for (int w = 0; w < NWC; ++w) o += f[w] != 0.f ? f[w] * so[w][e] : 0.f;
-        out[e] = __float2bfloat16_rn(gated(p, b, hq, e, o / l));
+        out[e] = __float2bfloat16_rn(gate_apply(p.gate_mode, z[k], o / l));
     }
 }
 
