@@ -119,14 +119,14 @@ struct WorkSplit {
     }
 };
 
-// Fills `q` for the whole batch; all threads.
+// Fills `q` for the whole batch; all threads.  first_len: the length of sequence threadIdx.x.
 template <int D>
-__device__ void scan_batch(const int32_t* seqlens, int B, int Lmax, const Sequences& q, int* red) {
+__device__ void scan_batch(const int32_t* seqlens, int first_len, int B, int Lmax, const Sequences& q, int* red) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) q.tiles[0] = q.live[0] = 0;
     int tiles0 = 0, live0 = 0;
     for (int first = 0; first < B; first += THREADS) {
-        const int i = first + tid, L = i < B ? seqlens[i] : 0;
+        const int i = first + tid, L = first == 0 ? first_len : i < B ? seqlens[i] : 0;
         int v = seq_tiles<D>(L, Lmax);
         const uint32_t any = __ballot_sync(0xffffffffu, v > 0);
         const int n = __popc(any & ((2u << lane) - 1u));
@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     uint8_t* ring = smem + warp * n_stages * C::STAGE_BYTES;
     const uint32_t bars = smem_u32(tail + C::OFF_BAR) + warp * 8 * C::MAX_STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
+    const int first_len = (int)threadIdx.x < p.B ? p.seqlens[threadIdx.x] : 0;
     pdl_launch_dependents();  // the combine kernel may become resident; it waits for this grid to finish
 
     if (lane == 0) {
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     // heads and (in the sums) groups that do not exist stay zero
     for (int i = threadIdx.x + (r < 8 ? 0 : C::OFF_QSUM / 16); i < C::OFF_ML / 16; i += THREADS)
         reinterpret_cast<uint4*>(tail)[i] = make_uint4(0, 0, 0, 0);
-    scan_batch<D>(p.seqlens, p.B, Lmax, seqs, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
+    scan_batch<D>(p.seqlens, first_len, p.B, Lmax, seqs, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
 
     const WorkSplit split(p.G * (seqs.tiles[p.B] + kPieceTiles * seqs.live[p.B]), gridDim.x);
     if ((int)blockIdx.x >= split.N) return;
@@ -803,8 +804,12 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 // the warps meet in shared memory.  A sequence of length 0 gets the gate of an empty sum.
 template <int D, int NWC>
 __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_constant__ QcacheDecodeParams p, int n_ctas) {
-    constexpr int DPL = D / 32, CH = NWC == 8 ? 8 : 4, EPT = (D + 32 * NWC - 1) / (32 * NWC);
-    __shared__ float sm[NWC][2], so[NWC][D];
+    constexpr int DPL = D / 32, VEC = DPL < 4 ? DPL : 4, CH = NWC == 8 ? 8 : 4, EPT = (D + 32 * NWC - 1) / (32 * NWC);
+    struct alignas(4 * VEC) Vec {
+        float v[VEC];
+    };
+    __shared__ float sm[NWC][2];
+    __shared__ __align__(16) float so[NWC][D];
     __shared__ int units[NWC][2];
     const int b = blockIdx.x / p.H, hq = blockIdx.x % p.H;
     const int r = p.H / p.G, g = hq / r, h = hq % r, Lmax = p.max_pages * p.page_size;
@@ -874,7 +879,12 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
             ms[j] = live ? ps[r * D + h] : -INFINITY;
             ls[j] = live ? ps[r * D + r + h] : 0.f;
 #pragma unroll
-            for (int k = 0; k < DPL; ++k) os[j][k] = live ? ps[h * D + lane + 32 * k] : 0.f;
+            for (int k = 0; k < DPL / VEC; ++k) {
+                Vec x = {};
+                if (live) x = reinterpret_cast<const Vec*>(ps + h * D)[lane + 32 * k];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) os[j][k * VEC + i] = x.v[i];
+            }
         }
         float mx = m_run;
 #pragma unroll
@@ -898,7 +908,12 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
         sm[warp][1] = den;
     }
 #pragma unroll
-    for (int k = 0; k < DPL; ++k) so[warp][lane + 32 * k] = num[k];
+    for (int k = 0; k < DPL / VEC; ++k) {
+        Vec x;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x.v[i] = num[k * VEC + i];
+        reinterpret_cast<Vec*>(so[warp])[lane + 32 * k] = x;
+    }
     __syncthreads();
     float mx = -INFINITY, l = 0.f, f[NWC];
 #pragma unroll
