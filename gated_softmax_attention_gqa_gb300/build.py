@@ -52,7 +52,7 @@ def _binding_compile(obj):
 def _binding_link(obj, to):
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    return ["g++", "-shared", "-o", to, obj, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    return ["g++", "-shared", "-o", to, obj, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
             f"-L{HERE}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
 
 
