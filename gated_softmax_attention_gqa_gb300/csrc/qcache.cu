@@ -29,43 +29,40 @@ struct Vec16 {
     float2 p[8];
 };
 
-// A row's sixteen features as loaded.
+// Sixteen-byte chunk m of a warp's staged rows lies at chunk m ^ swizzle(m), so that the
+// eight lanes of a 128-byte access, which skip every other 16 features, meet all banks.
 template <typename T>
-struct Row16;
-template <>
-struct Row16<bf16> {
-    uint4 v[2];
-    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0, 0, 0, 0); }
-    // run c (0 or 1) from p
-    __device__ __forceinline__ void load8(int c, const bf16* p) { v[c] = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void get(Vec16& x) const {
+__device__ __forceinline__ int staged(int m) {
+    return sizeof(T) == 2 ? m ^ ((m >> 2) & 2) : m ^ (((m >> 3) & 1) | ((m >> 2) & 4));
+}
+
+// A lane's run c (0 or 1) of eight features, from chunk m of the staged rows on.
+__device__ __forceinline__ void load8(Vec16& x, int c, const uint4* rows, int m, bf16) {
+    const uint4 v = rows[staged<bf16>(m)];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+    for (int q = 0; q < 2; ++q) {
+        x.p[4 * c + 2 * q] = make_float2(bf16_lo(w[2 * q]), bf16_lo(w[2 * q + 1]));
+        x.p[4 * c + 2 * q + 1] = make_float2(bf16_hi(w[2 * q]), bf16_hi(w[2 * q + 1]));
+    }
+}
+__device__ __forceinline__ void load8(Vec16& x, int c, const uint4* rows, int m, float) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                x.p[4 * c + 2 * q] = make_float2(bf16_lo(w[2 * q]), bf16_lo(w[2 * q + 1]));
-                x.p[4 * c + 2 * q + 1] = make_float2(bf16_hi(w[2 * q]), bf16_hi(w[2 * q + 1]));
-            }
-        }
+    for (int q = 0; q < 2; ++q) {
+        const float4 v = reinterpret_cast<const float4*>(rows)[staged<float>(m + q)];
+        x.p[4 * c + 2 * q] = make_float2(v.x, v.z);
+        x.p[4 * c + 2 * q + 1] = make_float2(v.y, v.w);
     }
-};
-template <>
-struct Row16<float> {
-    float4 v[4];
-    __device__ __forceinline__ void zero() { v[0] = v[1] = v[2] = v[3] = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void load8(int c, const float* p) {
-        v[2 * c] = reinterpret_cast<const float4*>(p)[0];
-        v[2 * c + 1] = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void get(Vec16& x) const {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            x.p[2 * q] = make_float2(v[q].x, v[q].z);
-            x.p[2 * q + 1] = make_float2(v[q].y, v[q].w);
-        }
-    }
-};
+}
+
+__device__ __forceinline__ void copy16(uint4* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -216,102 +213,137 @@ __device__ __forceinline__ void encode_store(const Vec16 (&x)[2], uint8_t* block
     }
 }
 
+// Shared memory of a write block.
+template <typename T, int TEAM>
+struct WriteShared {
+    static constexpr int kStages = 2, kChunks = 512 * sizeof(T) / 16;  // a warp's pass: 512 features each of K and V
+    // What K' = (x wc + partner ws) / rms takes, products of the norm weights with cosine
+    // and sine (the rotation's sign in ws): quads of wc in rows 0-3, of ws in rows 4-7, a
+    // float4 a lane in Vec16 order.  The spare two spread a token's features, 32 at a time,
+    // over the banks.  In shared memory rather than in registers, because the kernel
+    // lives on warps per SM (with 16 of them it moved 2.9 TB/s, whatever the instructions).
+    float4 factors[kWarps / TEAM][8][34];
+    float4 plain[4][34];  // wc of features that are not turned: the norm weights, [quad][lane of the token]
+    float weights[256];
+    uint4 rows[kWarps][kStages][2][kChunks];  // K and V as copied, ahead of their use
+};
+
 // A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass.  `TEAM` of the block's
 // warps (one or all) take the same tokens, `passes` passes of them, and every TEAM-th of the
-// heads [blockIdx.y heads, ...); they make the sines and cosines together.
+// heads [blockIdx.y heads, ...); they make the factors together.  A warp's rows are copied to
+// shared memory two heads ahead.
 template <int D, typename T, int TEAM>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 6 : 4)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
-    constexpr int LPR = D / 16, TPW = 32 / LPR;
-    // sines and cosines of a pass, {sin, cos} of frequencies 2u, 2u + 1 in element
-    // [token][u % 4][u / 4] (lanes of neighbouring features read neighbouring elements), and one
-    // element that turns nothing
-    __shared__ float4 tables[kWarps / TEAM][TPW * D / 4 + 1];
-    // norm weights, and the rotation partners' with the rotation's sign, in Vec16 order
-    __shared__ float4 weights[2][4][LPR];
-    // their products with cosine and sine for the pass's tokens: each lane's own 32 floats,
-    // here rather than in registers, because the kernel lives on warps per SM (with 16 of them
-    // it moved 2.9 TB/s, whatever the instructions per warp)
-    __shared__ float4 factors[kWarps][8][32];
+    using S = WriteShared<T, TEAM>;
+    constexpr int LPR = D / 16, TPW = 32 / LPR, EPC = 16 / sizeof(T), CPR = D / EPC, CPL = S::kChunks / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    S& sh = *reinterpret_cast<S*>(smem);
     pdl_launch_dependents();  // a decode step may set itself up; it waits for this grid before it reads the cache
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mate_id = warp % TEAM, tl = lane / LPR, lc = lane % LPR;
     const int t0 = (blockIdx.x * (kWarps / TEAM) + warp / TEAM) * TPW * passes;
     const int e0 = first_feature(lc), g0 = blockIdx.y * heads + mate_id, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
+    const int mine_heads = g0 < g1 ? (g1 - g0 + TEAM - 1) / TEAM : 0;
+    if (TEAM == 1) passes = min(passes, (p.T - t0 + TPW - 1) / TPW);
+
+    // ---- the copies: lane l takes chunks l, l + 32, ... of a pass's tokens, head after head
+    const int my_token = lane / CPR;
+    const T* kf = static_cast<const T*>(p.k) + (int64_t)(t0 + my_token) * p.k_tok_stride + g0 * p.k_head_stride + lane % CPR * EPC;
+    const T* vf = static_cast<const T*>(p.v) + (int64_t)(t0 + my_token) * p.v_tok_stride + g0 * p.v_head_stride + lane % CPR * EPC;
+    int left = passes * mine_heads, head_left = mine_heads, token = t0 + my_token;
+    auto fetch = [&](int stage) {
+        if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < CPL; ++i) {
+                // chunk 32 i + lane: CPR chunks a token
+                constexpr bool kWide = CPR > 32;
+                const int dt = kWide ? i / (CPR / 32) : i * (32 / CPR), de = kWide ? i % (CPR / 32) * 32 * EPC : 0;
+                const int at = staged<T>(32 * i + lane);
+                if (token + dt < p.T) {  // a token past the end keeps what the buffer holds; it is not stored
+                    copy16(&sh.rows[warp][stage][0][at], kf + dt * p.k_tok_stride + de);
+                    copy16(&sh.rows[warp][stage][1][at], vf + dt * p.v_tok_stride + de);
+                }
+            }
+            --left;
+            kf += TEAM * p.k_head_stride;
+            vf += TEAM * p.v_head_stride;
+            if (--head_left == 0) {
+                head_left = mine_heads;
+                token += TPW;
+                kf += TPW * p.k_tok_stride - mine_heads * (TEAM * p.k_head_stride);
+                vf += TPW * p.v_tok_stride - mine_heads * (TEAM * p.v_head_stride);
+            }
+        }
+        copies_commit();
+    };
+    fetch(0);
+    fetch(1);
+
     const int half = p.rd >> 1;
     // distance of the rotation partner, eight features at a time (half is a multiple of 8);
     // 0: features past rotary_dim, which are not turned
     auto partner = [&](int e) { return e < half ? half : e < p.rd ? -half : 0; };
-    const int mate[2] = {partner(e0), partner(e0 + 16)};
+    // float of feature e of token k within rows q of `factors` or `plain` (of a token's lanes)
+    auto place = [&](int e, int k) {
+        const int q = 2 * ((e >> 4) & 1) + ((e >> 2) & 1), of = 2 * (e >> 5) + ((e >> 3) & 1);
+        return (q * 34 + k * LPR + of) * 4 + (e & 1) * 2 + ((e >> 1) & 1);
+    };
+    for (int e = threadIdx.x; e < D; e += 32 * kWarps) {
+        const float w = to_float(static_cast<const T*>(p.knorm_w)[e]);
+        sh.weights[e] = w;
+        reinterpret_cast<float*>(sh.plain)[place(e, 0)] = w;
+    }
     Place mine;  // of token t0 + lane
     const bool ok = report(lane < passes * TPW ? place_new(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
 
-    for (int e = threadIdx.x; e < D; e += 32 * kWarps) {
-        // run, quad and place of feature e in its lane's Vec16
-        const int m = partner(e), q = 2 * ((e >> 4) & 1) + ((e >> 2) & 1), of = 2 * (e >> 5) + ((e >> 3) & 1);
-        const int at = (q * LPR + of) * 4 + (e & 1) * 2 + ((e >> 1) & 1);
-        const T* w = static_cast<const T*>(p.knorm_w);
-        reinterpret_cast<float*>(weights[0])[at] = to_float(w[e]);
-        reinterpret_cast<float*>(weights[1])[at] = m > 0 ? -to_float(w[e + m]) : to_float(w[e + m]);
-    }
-    float4* table = tables[warp / TEAM];
-    if (lane == 0) table[TPW * D / 4] = make_float4(0.f, 1.f, 0.f, 1.f);
-    const float4* sc[2];
-    int step[2];
+    float* const factors = reinterpret_cast<float*>(sh.factors[warp / TEAM]);
+    constexpr int kSines = 4 * 34 * 4;  // floats from a feature's wc to its ws
+    const int mate[2] = {partner(e0), partner(e0 + 16)};
+    const float4* wc[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int e = e0 + 16 * c;
-        sc[c] = table + (mate[c] ? tl * (half / 2) + (e < half ? e : e - half) / 8 : TPW * D / 4);
-        step[c] = mate[c] ? half / 8 : 0;
-    }
+    for (int c = 0; c < 2; ++c) wc[c] = mate[c] ? &sh.factors[warp / TEAM][2 * c][lane] : &sh.plain[2 * c][lc];
     const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
+    const int chunk0 = tl * CPR + e0 / EPC;
     __syncthreads();
 
+    int stage = 0;
     for (int pass = 0; pass < passes; ++pass) {
-        if (TEAM == 1 && t0 + pass * TPW >= p.T) break;
-        for (int k = mate_id; k < TPW; k += TEAM) {
-            const int pos = __shfl_sync(0xffffffffu, mine.pos, pass * TPW + k);
-            for (int i = lane; i < half; i += 32) {
+        for (int i0 = 0; i0 < half; i0 += 32) {
+            const int i = min(i0 + lane, half - 1);
+            const float wl = sh.weights[i], wh = sh.weights[i + half];
+            float* const lo = factors + place(i, 0);
+            float* const hi = factors + place(i + half, 0);
+            for (int k = mate_id; k < TPW; k += TEAM) {
+                const int pos = __shfl_sync(0xffffffffu, mine.pos, pass * TPW + k);
                 float s, c;
                 rope_turn_sincos(p.turns[i], pos, &s, &c);
-                reinterpret_cast<float2*>(table + k * (half / 2) + ((i >> 1) & 3) * (half / 8) + (i >> 3))[i & 1] =
-                    make_float2(s, c);
+                if (i0 + lane < half) {
+                    lo[k * LPR * 4] = wl * c;
+                    hi[k * LPR * 4] = wh * c;
+                    lo[k * LPR * 4 + kSines] = -wh * s;
+                    hi[k * LPR * 4 + kSines] = wl * s;
+                }
             }
         }
         if (TEAM > 1) __syncthreads(); else __syncwarp();
-        // K' = (x wc + partner ws) / rms
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 w = weights[0][q][lc], m = weights[1][q][lc];
-            const float4 a = sc[q >> 1][(2 * q & 3) * step[q >> 1]], b = sc[q >> 1][((2 * q & 3) + 1) * step[q >> 1]];
-            const float2 c0 = mul2(make_float2(w.x, w.y), make_float2(a.y, b.y));
-            const float2 c1 = mul2(make_float2(w.z, w.w), make_float2(a.w, b.w));
-            const float2 s0 = mul2(make_float2(m.x, m.y), make_float2(a.x, b.x));
-            const float2 s1 = mul2(make_float2(m.z, m.w), make_float2(a.z, b.z));
-            factors[warp][q][lane] = make_float4(c0.x, c0.y, c1.x, c1.y);
-            factors[warp][4 + q][lane] = make_float4(s0.x, s0.y, s1.x, s1.y);
-        }
-        if (TEAM > 1) __syncthreads(); else __syncwarp();  // the next pass overwrites the table
         const Place at = place_of(mine, pass * TPW + tl);
         const bool live = at.page >= 0;
         uint8_t* block = p.cache + (live ? (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) : 0);
         const int row = at.slot % kQcBlock;
-        const int64_t t = min(t0 + pass * TPW + tl, p.T - 1);
-        const T* kp = static_cast<const T*>(p.k) + t * p.k_tok_stride + g0 * p.k_head_stride + e0;
-        const T* vp = static_cast<const T*>(p.v) + t * p.v_tok_stride + g0 * p.v_head_stride + e0;
         for (int g = g0; g < g1; g += TEAM) {
-            Row16<T> kr, ko, vr;
-            ko.zero();
+            copies_wait<S::kStages - 1>();
+            __syncwarp();
+            const uint4* kr = sh.rows[warp][stage][0];
+            const uint4* vr = sh.rows[warp][stage][1];
+            Vec16 x[2], o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o.p[i] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                kr.load8(c, kp + 16 * c);
-                if (mate[c]) ko.load8(c, kp + 16 * c + mate[c]);
-                vr.load8(c, vp + 16 * c);
+                load8(x[0], c, kr, chunk0 + c * 16 / EPC, T());
+                if (mate[c]) load8(o, c, kr, chunk0 + (c * 16 + mate[c]) / EPC, T());
             }
-            kp += TEAM * p.k_head_stride;
-            vp += TEAM * p.v_head_stride;
-            Vec16 x[2], o;
-            kr.get(x[0]);
             float2 s2 = mul2(x[0].p[0], x[0].p[0]);
 #pragma unroll
             for (int i = 1; i < 8; ++i) s2 = fma2(x[0].p[i], x[0].p[i], s2);
@@ -319,19 +351,25 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 6 : 4)
 #pragma unroll
             for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
             const float2 rinv = both(inv_sqrt(ss / (float)D + p.eps));
-            ko.get(o);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float4 wc = factors[warp][q][lane], ws = factors[warp][4 + q][lane];
-                x[0].p[2 * q] = mul2(fma2(x[0].p[2 * q], make_float2(wc.x, wc.y), mul2(o.p[2 * q], make_float2(ws.x, ws.y))), rinv);
+                const float4 w = wc[q >> 1][(q & 1) * 34];
+                float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (mate[q >> 1]) m = wc[q >> 1][(q & 1) * 34 + kSines / 4];
+                x[0].p[2 * q] = mul2(fma2(x[0].p[2 * q], make_float2(w.x, w.y), mul2(o.p[2 * q], make_float2(m.x, m.y))), rinv);
                 x[0].p[2 * q + 1] =
-                    mul2(fma2(x[0].p[2 * q + 1], make_float2(wc.z, wc.w), mul2(o.p[2 * q + 1], make_float2(ws.z, ws.w))), rinv);
+                    mul2(fma2(x[0].p[2 * q + 1], make_float2(w.z, w.w), mul2(o.p[2 * q + 1], make_float2(m.z, m.w))), rinv);
             }
-            vr.get(x[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) load8(x[1], c, vr, chunk0 + c * 16 / EPC, T());
+            __syncwarp();
+            fetch(stage);
+            stage ^= 1;
             encode_store(x, block, plane, row, lc, D, live);
             block += TEAM * head;
         }
     }
+    copies_wait<0>();
 }
 
 // Eight stored features (their nibbles lowest first) as bf16 or fp32.  bf16: a nibble or-ed
@@ -435,7 +473,11 @@ cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) 
     const Cut c = cut_of<D>(p.T, p.G, 4);
     auto kernel = fp32 ? (c.team > 1 ? qcache_write_kernel<D, float, kWarps> : qcache_write_kernel<D, float, 1>)
                        : (c.team > 1 ? qcache_write_kernel<D, bf16, kWarps> : qcache_write_kernel<D, bf16, 1>);
-    kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads);
+    const size_t shared = fp32 ? (c.team > 1 ? sizeof(WriteShared<float, kWarps>) : sizeof(WriteShared<float, 1>))
+                               : (c.team > 1 ? sizeof(WriteShared<bf16, kWarps>) : sizeof(WriteShared<bf16, 1>));
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), 227 * 1024);
+    if (e != cudaSuccess) return e;
+    kernel<<<c.grid, 32 * kWarps, shared, stream>>>(p, c.passes, c.heads);
     return cudaGetLastError();
 }
 
