@@ -155,9 +155,10 @@ __device__ __forceinline__ bool report(int what, unsigned int* status) {
 // Quantise this lane's features of K and of V (neighbouring lanes share a group of 32, four
 // a slab) and store them at row `row` of `block` and of the V plane's block.  The two go
 // together so that one's chain of extremes, scale and reciprocal fills the other's waits.
-// All lanes of the warp.
-__device__ __forceinline__ void encode_store(const Vec16 (&x)[2], uint8_t* block, int64_t plane, int row, int lc, int d,
-                                             bool live) {
+// K is x[0] * rinv: its group's centre and reciprocal scale are taken to x[0]'s measure
+// (rms = 1 / rinv) instead of sixteen numbers to the group's.  All lanes of the warp.
+__device__ __forceinline__ void encode_store(const Vec16 (&x)[2], float rinv, float rms, uint8_t* block, int64_t plane,
+                                             int row, int lc, int d, bool live) {
     float hi[2], lo[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -178,7 +179,11 @@ __device__ __forceinline__ void encode_store(const Vec16 (&x)[2], uint8_t* block
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        q[n] = qc_group(lo[n], hi[n]);
+        q[n] = n ? qc_group(lo[n], hi[n]) : qc_group(lo[n] * rinv, hi[n] * rinv);
+        if (n == 0) {
+            q[n].centre *= rms;
+            q[n].inv *= rinv;
+        }
         const float2 ends = fma2(add2(make_float2(lo[n], hi[n]), both(-q[n].centre)), both(q[n].inv), both(kQcMagic + 8.f));
         inside = inside && ends.x >= kQcMagic && ends.y <= kQcMagic + 15.f;
     }
@@ -223,7 +228,7 @@ struct WriteShared {
     // over the banks.  In shared memory rather than in registers, because the kernel
     // lives on warps per SM (with 16 of them it moved 2.9 TB/s, whatever the instructions).
     float4 factors[kWarps / TEAM][8][34];
-    float4 plain[4][34];  // wc of features that are not turned: the norm weights, [quad][lane of the token]
+    float4 plain[8][34];  // the same of features that are not turned (the norm weights, and zeros), a token's lanes
     float weights[256];
     uint4 rows[kWarps][kStages][2][kChunks];  // K and V as copied, ahead of their use
 };
@@ -288,6 +293,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
         const int q = 2 * ((e >> 4) & 1) + ((e >> 2) & 1), of = 2 * (e >> 5) + ((e >> 3) & 1);
         return (q * 34 + k * LPR + of) * 4 + (e & 1) * 2 + ((e >> 1) & 1);
     };
+    for (int i = threadIdx.x; i < 4 * 34; i += 32 * kWarps) sh.plain[4][i] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int e = threadIdx.x; e < D; e += 32 * kWarps) {
         const float w = to_float(static_cast<const T*>(p.knorm_w)[e]);
         sh.weights[e] = w;
@@ -305,6 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     for (int c = 0; c < 2; ++c) wc[c] = mate[c] ? &sh.factors[warp / TEAM][2 * c][lane] : &sh.plain[2 * c][lc];
     const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
     const int chunk0 = tl * CPR + e0 / EPC;
+    const int chunk_o[2] = {chunk0 + mate[0] / EPC, chunk0 + (16 + mate[1]) / EPC};  // the partners'
     __syncthreads();
 
     int stage = 0;
@@ -338,11 +345,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
             const uint4* vr = sh.rows[warp][stage][1];
             Vec16 x[2], o;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o.p[i] = make_float2(0.f, 0.f);
-#pragma unroll
             for (int c = 0; c < 2; ++c) {
                 load8(x[0], c, kr, chunk0 + c * 16 / EPC, T());
-                if (mate[c]) load8(o, c, kr, chunk0 + (c * 16 + mate[c]) / EPC, T());
+                load8(o, c, kr, chunk_o[c], T());
             }
             float2 s2 = mul2(x[0].p[0], x[0].p[0]);
 #pragma unroll
@@ -350,22 +355,19 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
             float ss = s2.x + s2.y;
 #pragma unroll
             for (int s = LPR / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-            const float2 rinv = both(inv_sqrt(ss / (float)D + p.eps));
+            const float ms = ss / (float)D + p.eps, rinv = inv_sqrt(ms);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float4 w = wc[q >> 1][(q & 1) * 34];
-                float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (mate[q >> 1]) m = wc[q >> 1][(q & 1) * 34 + kSines / 4];
-                x[0].p[2 * q] = mul2(fma2(x[0].p[2 * q], make_float2(w.x, w.y), mul2(o.p[2 * q], make_float2(m.x, m.y))), rinv);
-                x[0].p[2 * q + 1] =
-                    mul2(fma2(x[0].p[2 * q + 1], make_float2(w.z, w.w), mul2(o.p[2 * q + 1], make_float2(m.z, m.w))), rinv);
+                const float4 w = wc[q >> 1][(q & 1) * 34], m = wc[q >> 1][(q & 1) * 34 + kSines / 4];
+                x[0].p[2 * q] = fma2(x[0].p[2 * q], make_float2(w.x, w.y), mul2(o.p[2 * q], make_float2(m.x, m.y)));
+                x[0].p[2 * q + 1] = fma2(x[0].p[2 * q + 1], make_float2(w.z, w.w), mul2(o.p[2 * q + 1], make_float2(m.z, m.w)));
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) load8(x[1], c, vr, chunk0 + c * 16 / EPC, T());
             __syncwarp();
             fetch(stage);
             stage ^= 1;
-            encode_store(x, block, plane, row, lc, D, live);
+            encode_store(x, rinv, ms * rinv, block, plane, row, lc, D, live);
             block += TEAM * head;
         }
     }
