@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     copies_wait<0>();
 }
 
-// Eight stored features (their nibbles lowest first) as bf16 or fp32.  bf16: a nibble or-ed
+// Eight stored features (their nibbles lowest first) as bf16, or four and four, eight apart, as fp32.  bf16: a nibble or-ed
 // into 128's mantissa reads as 128 + code; the difference to 136 is exact and the fused
 // multiply-add rounds centre + scale (code - 8) once.
 __device__ __forceinline__ void decode8(uint32_t n, uint32_t s2, uint32_t c2, bf16* out) {
@@ -396,17 +396,26 @@ __device__ __forceinline__ void decode8(uint32_t n, uint32_t s2, uint32_t c2, fl
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = fmaf(s, __uint_as_float(((n >> (4 * k)) & 15u) | 0x4B000000u) - 8388616.f, c);
     reinterpret_cast<float4*>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    reinterpret_cast<float4*>(out)[2] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// The same layout of work: a lane reads back 16 features of one token, head after head.
+__device__ __forceinline__ uint2 load_run(const uint8_t* p, bf16) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ uint2 load_run(const uint8_t* p, float) {
+    return make_uint2(reinterpret_cast<const uint32_t*>(p)[0], reinterpret_cast<const uint32_t*>(p)[2]);
+}
+
+// The same layout of work: a lane reads back 16 features of one token, head after head; fp32
+// in four runs of four, so that here too each store of two neighbours fills whole sectors
+// (with runs of eight, stored in halves, 6 sequences of 0-4099 tokens, 8 x 64, took 17.0 us).
 template <int D, typename T>
 __global__ void __launch_bounds__(32 * kWarps)
     qcache_read_kernel(const __grid_constant__ QcacheReadParams p, int passes, int heads, int team) {
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t0 = (blockIdx.x * (kWarps / team) + warp / team) * TPW * passes;
-    const int lc = lane % LPR, e0 = first_feature(lc), g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
+    constexpr int RUN = 16 / sizeof(T);  // features of a run
+    const int lc = lane % LPR, e0 = first_feature(lc) - (8 - RUN) * (lc & 1);
+    const int g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
     if (t0 >= p.T || g0 >= g1) return;
     Place mine;  // of token t0 + lane
     const bool ok = report(lane < passes * TPW ? place_cached(p, t0 + lane, mine) : kSkip, p.status);
@@ -418,7 +427,7 @@ __global__ void __launch_bounds__(32 * kWarps)
         if (at.page < 0) continue;  // no lane of this token goes on; the shuffles above are whole again next time
         const int64_t t = t0 + pass * TPW + lane / LPR;
         const int row = at.slot % kQcBlock;
-        const int codes = (lc >> 2) * 512 + row * 32 + 8 * (lc & 1);
+        const int codes = (lc >> 2) * 512 + row * 32 + RUN * (lc & 1);
         const uint8_t* src = p.cache + (at.page * (int64_t)p.G + g0) * head + (at.slot / kQcBlock) * qc_block_bytes(D) + codes;
         const int par = 8 * D + ((lc >> 1) * 16 + row) * 2 - codes;
         T* kout = static_cast<T*>(p.k) + (t * p.G + g0) * D + e0;
@@ -429,8 +438,8 @@ __global__ void __launch_bounds__(32 * kWarps)
             uint32_t s[2], c[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // K and V
-                w[i][0] = *reinterpret_cast<const uint2*>(src + i * plane);
-                w[i][1] = *reinterpret_cast<const uint2*>(src + i * plane + 16);
+                w[i][0] = load_run(src + i * plane, T());
+                w[i][1] = load_run(src + i * plane + 16, T());
                 s[i] = *reinterpret_cast<const uint16_t*>(src + i * plane + par);
                 c[i] = *reinterpret_cast<const uint16_t*>(src + i * plane + par + D);
             }
@@ -458,13 +467,13 @@ struct Cut {
     dim3 grid;
 };
 template <int D>
-Cut cut_of(int T, int G, int passes) {
+Cut cut_of(int T, int G, int passes, int spread) {
     constexpr int TPW = 32 / (D / 16);
     const int64_t want = 8 * (int64_t)device_sm_count(), groups = ((int64_t)T + TPW - 1) / TPW;
     Cut c{passes, G, 1, dim3()};
     if (groups < passes * want) c.passes = 1;
     if (G > 1 && groups < want) c.team = kWarps;
-    while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < want) c.heads = (c.heads + 1) / 2;
+    while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < spread * want) c.heads = (c.heads + 1) / 2;
     const int tokens = kWarps / c.team * TPW * c.passes;
     c.grid = dim3((unsigned)((T + tokens - 1) / tokens), (unsigned)((G + c.heads - 1) / c.heads));
     return c;
@@ -472,7 +481,7 @@ Cut cut_of(int T, int G, int passes) {
 
 template <int D>
 cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G, 4);
+    const Cut c = cut_of<D>(p.T, p.G, 4, 1);
     auto kernel = fp32 ? (c.team > 1 ? qcache_write_kernel<D, float, kWarps> : qcache_write_kernel<D, float, 1>)
                        : (c.team > 1 ? qcache_write_kernel<D, bf16, kWarps> : qcache_write_kernel<D, bf16, 1>);
     const size_t shared = fp32 ? (c.team > 1 ? sizeof(WriteShared<float, kWarps>) : sizeof(WriteShared<float, 1>))
@@ -485,7 +494,7 @@ cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) 
 
 template <int D>
 cudaError_t read_d(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G, 2);
+    const Cut c = cut_of<D>(p.T, p.G, 2, 2);
     auto kernel = fp32 ? qcache_read_kernel<D, float> : qcache_read_kernel<D, bf16>;
     kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads, c.team);
     return cudaGetLastError();
