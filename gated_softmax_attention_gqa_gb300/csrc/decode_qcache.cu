@@ -397,8 +397,11 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     uint8_t* ring = smem + warp * n_stages * C::STAGE_BYTES;
     const uint32_t bars = smem_u32(tail + C::OFF_BAR) + warp * 8 * C::MAX_STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
-    const int first_len = (int)threadIdx.x < p.B ? p.seqlens[threadIdx.x] : 0;
+    // After a write of the appended rows everything but the cache is ready: that kernel
+    // lets this one start only once those ahead of it have finished.
+    if (!after_write) pdl_wait_prerequisites();
     pdl_launch_dependents();  // the combine kernel may become resident; it waits for this grid to finish
+    const int first_len = (int)threadIdx.x < p.B ? p.seqlens[threadIdx.x] : 0;
 
     if (lane == 0) {
         for (int s = 0; s < n_stages; ++s) mbar_init(bars + 8 * s, 1);
@@ -945,32 +948,18 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
     stages = stages < 2 ? 2 : stages > C::MAX_STAGES ? C::MAX_STAGES : stages;
     cudaError_t e = set_smem_once(reinterpret_cast<const void*>(qdecode_split_kernel<D>), 227 * 1024);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.stream = stream;
-    cfg.gridDim = dim3((unsigned)n_ctas);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = (size_t)(NW * stages * C::STAGE_BYTES + tail);
-    cfg.numAttrs = after_write ? 1 : 0;
     if (ev_start) cudaEventRecord(ev_start, stream);
-    e = cudaLaunchKernelEx(&cfg, qdecode_split_kernel<D>, p, stages, after_write);
+    e = launch_early(qdecode_split_kernel<D>, dim3((unsigned)n_ctas), dim3(THREADS),
+                     (size_t)(NW * stages * C::STAGE_BYTES + tail), stream, p, stages, after_write);
     if (ev_stop) cudaEventRecord(ev_stop, stream);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(p.B * p.H));
-    cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
     // Eight warps share a head's states where a sequence may be spread over many CTAs, two
     // where there are about as many (sequence, KV head) pairs as CTAs and so a state or two
     // each (200 sequences of 0-300 tokens, 4 x 3 heads: 18.0 us with two warps, 21.0 with eight).
-    if ((int64_t)p.B * p.G * 2 <= n_ctas) {
-        cfg.blockDim = dim3(256);
-        return cudaLaunchKernelEx(&cfg, qdecode_combine_kernel<D, 8>, p, n_ctas);
-    }
-    cfg.blockDim = dim3(64);
-    return cudaLaunchKernelEx(&cfg, qdecode_combine_kernel<D, 2>, p, n_ctas);
+    const dim3 heads((unsigned)(p.B * p.H));
+    if ((int64_t)p.B * p.G * 2 <= n_ctas)
+        return launch_early(qdecode_combine_kernel<D, 8>, heads, dim3(256), 0, stream, p, n_ctas);
+    return launch_early(qdecode_combine_kernel<D, 2>, heads, dim3(64), 0, stream, p, n_ctas);
 }
 
 }  // namespace

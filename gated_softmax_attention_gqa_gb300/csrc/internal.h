@@ -162,6 +162,7 @@ struct QcacheWriteParams {
     int num_pages, page_size, max_pages;
     PageDiv by_page;
     int T, B, G, d, rd;
+    bool before_decode;  // the kernel launched next may be placed early
     float eps;
     unsigned int* status;
     uint64_t turns[kMaxRotaryHalf];

@@ -244,7 +244,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     constexpr int LPR = D / 16, TPW = 32 / LPR, EPC = 16 / sizeof(T), CPR = D / EPC, CPL = S::kChunks / 32;
     extern __shared__ __align__(16) uint8_t smem[];
     S& sh = *reinterpret_cast<S*>(smem);
-    pdl_launch_dependents();  // a decode step may set itself up; it waits for this grid before it reads the cache
+    pdl_wait_prerequisites();  // the kernel ahead may not have finished when this one is placed
+    // a decode step sets itself up meanwhile, and waits before it reads the cache
+    if (p.before_decode) pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mate_id = warp % TEAM, tl = lane / LPR, lc = lane % LPR;
     const int t0 = (blockIdx.x * (kWarps / TEAM) + warp / TEAM) * TPW * passes;
     const int e0 = first_feature(lc), g0 = blockIdx.y * heads + mate_id, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     constexpr int LPR = D / 16, TPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t0 = (blockIdx.x * (kWarps / team) + warp / team) * TPW * passes;
+    pdl_wait_prerequisites();
     constexpr int RUN = 16 / sizeof(T);  // features of a run
     const int lc = lane % LPR, e0 = first_feature(lc) - (8 - RUN) * (lc & 1);
     const int g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
@@ -488,16 +491,14 @@ cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) 
                                : (c.team > 1 ? sizeof(WriteShared<bf16, kWarps>) : sizeof(WriteShared<bf16, 1>));
     const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), 227 * 1024);
     if (e != cudaSuccess) return e;
-    kernel<<<c.grid, 32 * kWarps, shared, stream>>>(p, c.passes, c.heads);
-    return cudaGetLastError();
+    return launch_early(kernel, c.grid, dim3(32 * kWarps), shared, stream, p, c.passes, c.heads);
 }
 
 template <int D>
 cudaError_t read_d(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
     const Cut c = cut_of<D>(p.T, p.G, 2, 2);
     auto kernel = fp32 ? qcache_read_kernel<D, float> : qcache_read_kernel<D, bf16>;
-    kernel<<<c.grid, 32 * kWarps, 0, stream>>>(p, c.passes, c.heads, c.team);
-    return cudaGetLastError();
+    return launch_early(kernel, c.grid, dim3(32 * kWarps), 0, stream, p, c.passes, c.heads, c.team);
 }
 
 }  // namespace

@@ -67,20 +67,12 @@ bool row_strides_ok(const void* p, int64_t tok, int64_t head, int elt) {
     return aligned(p, 16) && tok >= 0 && head >= 0 && tok * elt % 16 == 0 && head * elt % 16 == 0;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t gattn_qcache_bytes(int num_pages, int G, int page_size, int d) {
-    if (num_pages < 1 || G < 1 || page_size < kQcBlock || page_size % kQcBlock || d < 64 || d % 64) return 0;
-    return (size_t)2 * num_pages * G * (page_size / kQcBlock) * (size_t)qc_block_bytes(d);
-}
-
-gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, const int32_t* block_table, int num_pages,
-                                int page_size, int max_pages, const int32_t* seqlens, const int32_t* cu_seqlens,
-                                const void* knorm_w, int T, int B, int G, int d, int rotary_dim, double rope_base,
-                                float eps, int64_t k_tok_stride, int64_t k_head_stride, int64_t v_tok_stride,
-                                int64_t v_head_stride, int dtype, void* stream) {
+// gattn_qcache_write; before_decode: a decode step's split kernel is launched next.
+gattn_status write_tokens(const void* k, const void* v, void* qcache, const int32_t* block_table, int num_pages,
+                          int page_size, int max_pages, const int32_t* seqlens, const int32_t* cu_seqlens,
+                          const void* knorm_w, int T, int B, int G, int d, int rotary_dim, double rope_base,
+                          float eps, int64_t k_tok_stride, int64_t k_head_stride, int64_t v_tok_stride,
+                          int64_t v_head_stride, int dtype, void* stream, bool before_decode) {
     if (dtype != GATTN_BF16 && dtype != GATTN_FP32) return GATTN_ERR_INVALID_ARG;
     if (T < 0 || (!cu_seqlens && T != B)) return GATTN_ERR_INVALID_ARG;
     gattn_status st = check_pool(qcache, block_table, num_pages, page_size, max_pages, B, G, d);
@@ -120,11 +112,31 @@ gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, cons
     p.G = G;
     p.d = d;
     p.rd = rotary_dim;
+    p.before_decode = before_decode;
     p.eps = eps;
     fill_turns(p.turns, rotary_dim, rope_base);
     return launch_qcache_write(p, dtype == GATTN_FP32, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GATTN_OK
                : GATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gattn_qcache_bytes(int num_pages, int G, int page_size, int d) {
+    if (num_pages < 1 || G < 1 || page_size < kQcBlock || page_size % kQcBlock || d < 64 || d % 64) return 0;
+    return (size_t)2 * num_pages * G * (page_size / kQcBlock) * (size_t)qc_block_bytes(d);
+}
+
+gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, const int32_t* block_table, int num_pages,
+                                int page_size, int max_pages, const int32_t* seqlens, const int32_t* cu_seqlens,
+                                const void* knorm_w, int T, int B, int G, int d, int rotary_dim, double rope_base,
+                                float eps, int64_t k_tok_stride, int64_t k_head_stride, int64_t v_tok_stride,
+                                int64_t v_head_stride, int dtype, void* stream) {
+    return write_tokens(k, v, qcache, block_table, num_pages, page_size, max_pages, seqlens, cu_seqlens, knorm_w, T, B, G,
+                        d, rotary_dim, rope_base, eps, k_tok_stride, k_head_stride, v_tok_stride, v_head_stride, dtype,
+                        stream, false);
 }
 
 gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, int num_pages, int page_size,
@@ -201,8 +213,8 @@ gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const voi
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return GATTN_ERR_WORKSPACE;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     if (append) {
-        st = gattn_qcache_write(k_new, v_new, qcache, block_table, num_pages, page_size, max_pages, seqlens, nullptr,
-                                knorm_w, B, B, G, d, rotary_dim, rope_base, eps, 0, 0, 0, 0, GATTN_BF16, stream_);
+        st = write_tokens(k_new, v_new, qcache, block_table, num_pages, page_size, max_pages, seqlens, nullptr,
+                          knorm_w, B, B, G, d, rotary_dim, rope_base, eps, 0, 0, 0, 0, GATTN_BF16, stream_, true);
         if (st != GATTN_OK) return st;
     }
     QcacheDecodeParams p;
