@@ -14,25 +14,29 @@
 //       end of a piece, where they are merged in shared memory.  (A producer warp for the
 //       four cost a fifth warp's registers, which the accumulators need: 128 a thread
 //       spilled, and 64 sequences of 16k-32k tokens took 432 us.)
-//         S^T = K Q^T   m16n8k16, fp16: sixteen keys by the H/G <= 8 queries.  Codes become
-//             fp16 operands without arithmetic: a nibble or-ed into the low mantissa bits
-//             of 1024 reads as 1024 + code (or 1024 + 16 code one nibble higher, with
-//             q / 16), and the accumulator starts at minus the constant's share, so it ends
-//             at sum q (code - 8) as if the operand had been code - 8.  Each group's sum is
-//             scaled once per key; the centres enter by one more product, centre_k . (sum
-//             of q over the group), q's sums split into two bf16 parts.  The weights turn
-//             into the next product's operand by a register transpose (movmatrix).
+//         S^T = K Q^T   m16n8k16, fp16: sixteen keys by the H/G <= 8 queries.  Numbers below
+//             2^-13 count in steps of 2^-24 in fp16, so a byte of two codes, zero-extended by
+//             one byte permute, is an fp16 operand as it stands, and so is its lower code,
+//             masked.  Upper codes are never taken apart: with byte = 16 upper + lower,
+//             q_l lower + q_u upper = (q_u / 16) byte + (q_l - q_u / 16) lower, and the
+//             queries are laid out as those two factors.  The accumulator starts at
+//             -8 sum q.  Each group's sum is scaled once per key; the centres enter by one
+//             more product, centre_k . (sum of q over the group), q's sums split into two
+//             bf16 parts.  The weights turn into the next product's operand by a register
+//             transpose (movmatrix).
 //         O^T += V^T P^T   m16n8k16, bf16.  The rows are features, so the pairs an operand
 //             register holds are two keys of one feature: two words of neighbouring keys
-//             are interleaved by bytes.  A bf16 below 2^-125 counts in steps of 2^-133, so a
-//             byte's nibbles, masked, are bf16 numbers as they stand, and one multiply-add by
-//             2^127 makes them (code - 8) / 64 and (code - 8) / 4, exact; the output's
-//             rows are multiplied up at the end.  (With nibbles shifted down one by one and
-//             or-ed into 128, the shifts held the ALU: 64 sequences of 16k-32k tokens, d = 256,
-//             took 181 us, now 173; 4 of 60k-131k, d = 128, 55 us, now 53.)  The scales
-//             multiply P instead (they are per key and group), and the centres' part,
+//             are interleaved by halves, once, and their bytes and lower codes masked.  A
+//             bf16 below 2^-125 counts in steps of 2^-133; one multiply-add by 2^127 makes
+//             (byte - 136) / 64 and (lower - 8) / 64, exact, which are rows 8-15 and 0-7;
+//             the upper codes' sums are 4 times their difference, taken at the end.  The
+//             scales multiply P instead (they are per key and group), and the centres' part,
 //             sum_k p_k centre_k, is one product for all groups, in whose spare rows ones
 //             sum the weights.
+//       What the unpacking costs the ALU, which is the pipe that holds d = 128 back, decides:
+//       with every nibble shifted down and or-ed into a power of two (28 instructions for 16
+//       keys of a group) 64 sequences of 16k-32k tokens, d = 256, took 181 us and 4 of
+//       60k-131k, d = 128, 55 us; with bytes and lower codes (18) 168 and 49.
 //   qdecode_combine_kernel  merges the partial states of pieces that several CTAs share
 //       and applies the gate; a (sequence, KV head) that one CTA covered is finished by
 //       that CTA.
@@ -48,6 +52,8 @@ constexpr int THREADS = 32 * NW;
 // What starting and merging a (sequence, KV head) piece costs, in tiles: the work split
 // counts it, so a CTA with many short sequences gets fewer tiles.
 constexpr int kPieceTiles = 2;
+// What a code of one is worth as an operand of the K product: the lowest fp16 bit.
+constexpr float kCode = 1.f / 16777216.f;
 
 template <int D>
 struct QdCfg {
@@ -206,18 +212,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
-// (x & MASK) | bits in one instruction; `bits` has to come from a register (opaque below),
-// since an instruction takes one immediate.
-template <uint32_t MASK>
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t bits) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(MASK), "r"(bits));
-    return d;
-}
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-    asm volatile("" : "+r"(x));
-    return x;
-}
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile(
@@ -352,33 +346,34 @@ __device__ void make_queries(const QcacheDecodeParams& p, int b, int g, int pos,
         const bool plain = ex == 0 || ex == 255;
         const float down = plain ? 1.f : __uint_as_float((uint32_t)min(max(253 - ex, 1), 254) << 23);
         const float up = plain ? 1.f : 1.f / down;
-        float cinit = 0.f, qsum = 0.f;
+        // a byte of two codes is met as itself and as its lower code alone, so q of the upper
+        // code, over 16, multiplies the byte and is taken off the lower one's
+        float qsum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool high = i & 1;  // codes 1, 3, 5, 7 of a word are met as 1024 + 16 code
-            const float y = round_f16(x[i] * down * (high ? 0.0625f : 1.f));
-            x[i] = y;
-            cinit -= (high ? 1152.f : 1032.f) * y;
-            qsum += (high ? 16.f : 1.f) * y;
+        for (int i = 0; i < 8; i += 2) {
+            const float upper = round_f16(x[i + 1] * down * 0.0625f), lower = round_f16(x[i] * down - upper);
+            x[i] = lower;
+            x[i + 1] = upper;
+            qsum += lower + 17.f * upper;  // the lower code's factor and 16 upper
         }
+        qsum *= kCode;
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
-            cinit += __shfl_xor_sync(0xffffffffu, cinit, o);
             qsum += __shfl_xor_sync(0xffffffffu, qsum, o);
         }
         if (live) {
             const int grp = u >> 2, t = u & 3;
             reinterpret_cast<uint4*>(tail + C::OFF_QF)[grp * 32 + h * 4 + t] =
-                make_uint4(pack_f16x2(x[0], x[4]), pack_f16x2(x[1], x[5]), pack_f16x2(x[2], x[6]), pack_f16x2(x[3], x[7]));
+                make_uint4(pack_f16x2(x[1], x[3]), pack_f16x2(x[0], x[2]), pack_f16x2(x[5], x[7]), pack_f16x2(x[4], x[6]));
             if (t == 0) {
                 float* ci = reinterpret_cast<float*>(tail + C::OFF_CINIT) + (grp * 4 + (h >> 1)) * 4 + (h & 1);
-                ci[0] = ci[2] = cinit;
+                ci[0] = ci[2] = -8.f * qsum;
                 bf16* qs = reinterpret_cast<bf16*>(tail + C::OFF_QSUM);
                 const bf16 hi = __float2bfloat16_rn(qsum);
                 qs[h * 8 + grp] = hi;
                 qs[64 + h * 8 + grp] = __float2bfloat16_rn(qsum - __bfloat162float(hi));
             }
-            if (u == 0) reinterpret_cast<float*>(tail + C::OFF_QSC)[h] = p.scale_log2 * up;
+            if (u == 0) reinterpret_cast<float*>(tail + C::OFF_QSC)[h] = p.scale_log2 * (up / kCode);
         }
     }
     __syncthreads();
@@ -504,9 +499,9 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     // V words are read so that the four lanes of a quad touch different banks: the upper
     // two take the pair's second key first, and the interleave undoes it
     const int kf = 2 * t + (t >> 1), ks = 2 * t + 1 - (t >> 1);
-    const uint32_t sel_lo = t < 2 ? 0x0400u : 0x0004u, sel_hi = t < 2 ? 0x0602u : 0x0206u;  // bytes 0 and 2
-    const uint32_t one_f16 = opaque(0x64006400u);  // 1024
-    constexpr uint32_t kUp = 0x7F007F00u, kMid64 = 0xBE00BE00u, kMid4 = 0xC000C000u;  // 2^127, -1/8, -2
+    const uint32_t sel_lo = t < 2 ? 0x5410u : 0x1054u, sel_hi = t < 2 ? 0x7632u : 0x3276u;
+    constexpr uint32_t kNibble = 0x000F000Fu, kByte = 0x00FF00FFu;
+    constexpr uint32_t kUp = 0x7F007F00u, kMid = 0xBE00BE00u, kMidByte = 0xC008C008u;  // 2^127, -8/64, -136/64
     int st = 0, done = 0;  // stage and number of the unit at hand
     uint32_t phase = 0;
     bool dead = false;
@@ -589,19 +584,14 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                         const int grp = 2 * sl + hf;
                         const uint4 qf = ld<uint4>(qfp + grp * 512);
                         const float4 ci = ld<float4>(cip + grp * 64);
-                        const uint32_t sel = hf ? 0x0602 : 0x0400;  // bytes 0 and 2 of the pair of halves
+                        const uint32_t sel = hf ? 0x4342 : 0x4140;  // the half's two bytes, zero-extended
 #pragma unroll
                         for (int n2 = 0; n2 < NB; ++n2) {
-                            const uint32_t c0 = __byte_perm(wa[n2].x, wa[n2].y, sel), c1 = __byte_perm(wb[n2].x, wb[n2].y, sel);
-                            const uint32_t d0 = __byte_perm(wa[n2].x, wa[n2].y, sel + 0x0101);
-                            const uint32_t d1 = __byte_perm(wb[n2].x, wb[n2].y, sel + 0x0101);
+                            const uint32_t x0 = __byte_perm(wa[n2].x, 0, sel), x1 = __byte_perm(wb[n2].x, 0, sel);
+                            const uint32_t y0 = __byte_perm(wa[n2].y, 0, sel), y1 = __byte_perm(wb[n2].y, 0, sel);
                             float a[4];
-                            mma_f16_16816(a, and_or<0x000F000Fu>(c0, one_f16), and_or<0x000F000Fu>(c1, one_f16),
-                                          and_or<0x00F000F0u>(c0, one_f16), and_or<0x00F000F0u>(c1, one_f16), qf.x, qf.y,
-                                          ci.x, ci.y, ci.z, ci.w);
-                            mma_f16_16816(a, and_or<0x000F000Fu>(d0, one_f16), and_or<0x000F000Fu>(d1, one_f16),
-                                          and_or<0x00F000F0u>(d0, one_f16), and_or<0x00F000F0u>(d1, one_f16), qf.z, qf.w,
-                                          a[0], a[1], a[2], a[3]);
+                            mma_f16_16816(a, x0, x1, x0 & kNibble, x1 & kNibble, qf.x, qf.y, ci.x, ci.y, ci.z, ci.w);
+                            mma_f16_16816(a, y0, y1, y0 & kNibble, y1 & kNibble, qf.z, qf.w, a[0], a[1], a[2], a[3]);
                             const uint8_t* kpn = kp + n2 * BB + grp * 32;
                             const float s0 = __uint_as_float((uint32_t)ld<uint16_t>(kpn) << 16);
                             const float s1 = __uint_as_float((uint32_t)ld<uint16_t>(kpn + 16) << 16);
@@ -687,18 +677,19 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                         for (int hf = 0; hf < 2; ++hf) {
                             const int grp = 2 * sl + hf;
                             const uint32_t sel = hf ? sel_hi : sel_lo;
-                            const uint32_t w0[2] = {__byte_perm(f0, s0, sel), __byte_perm(f0, s0, sel + 0x0101u)};
-                            const uint32_t w1[2] = {__byte_perm(f1, s1, sel), __byte_perm(f1, s1, sel + 0x0101u)};
+                            const uint32_t w0 = __byte_perm(f0, s0, sel), w1 = __byte_perm(f1, s1, sel);
+                            const uint32_t b0[2] = {w0 & kByte, __byte_perm(w0, 0, 0x4341)};
+                            const uint32_t b1[2] = {w1 & kByte, __byte_perm(w1, 0, 0x4341)};
                             const uint8_t* vpn = vp + n2 * BB + grp * 32;
                             const uint32_t p0 = mul_bf16x2(pr[n2][0], ld<uint32_t>(vpn));
                             const uint32_t p1 = mul_bf16x2(pr[n2][1], ld<uint32_t>(vpn + 16));
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                // (code - 8) / 64 in rows 0-7, (code - 8) / 4 in rows 8-15
-                                const uint32_t a0 = fma_bf16x2(w0[m] & 0x000F000Fu, kUp, kMid64);
-                                const uint32_t a1 = fma_bf16x2(w0[m] & 0x00F000F0u, kUp, kMid4);
-                                const uint32_t a2 = fma_bf16x2(w1[m] & 0x000F000Fu, kUp, kMid64);
-                                const uint32_t a3 = fma_bf16x2(w1[m] & 0x00F000F0u, kUp, kMid4);
+                                // (lower - 8) / 64 in rows 0-7, (byte - 136) / 64 in rows 8-15
+                                const uint32_t a0 = fma_bf16x2((m ? b0[1] : w0) & kNibble, kUp, kMid);
+                                const uint32_t a1 = fma_bf16x2(b0[m], kUp, kMidByte);
+                                const uint32_t a2 = fma_bf16x2((m ? b1[1] : w1) & kNibble, kUp, kMid);
+                                const uint32_t a3 = fma_bf16x2(b1[m], kUp, kMidByte);
                                 mma_bf16_16816(oacc[2 * grp + m], a0, a1, a2, a3, p0, p1);
                             }
                         }
@@ -760,7 +751,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     for (int e = 0; e < 2; ++e) {
                         if (f[e] != 0.f) {
                             o[i][e].x = fmaf(f[e], fmaf(64.f, oacc[m][e], e ? c1 : c0), o[i][e].x);
-                            o[i][e].y = fmaf(f[e], fmaf(4.f, oacc[m][2 + e], e ? c1 : c0), o[i][e].y);
+                            o[i][e].y = fmaf(f[e], fmaf(4.f, oacc[m][2 + e] - oacc[m][e], e ? c1 : c0), o[i][e].y);
                         }
                         if (2 * t + e < r) *place(m, e) = o[i][e];
                     }
