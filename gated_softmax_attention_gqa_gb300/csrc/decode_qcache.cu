@@ -6,12 +6,12 @@
 // numbers instead of half a one, and the instructions that unpack them decide how much
 // of the bandwidth is reached.
 //
-//   qdecode_split_kernel  persistent, a few CTAs of four warps per SM.  The (sequence, KV
-//       head) pairs are cut into tiles of 64 (d = 256) or 128 keys and the global tile list
-//       into equal contiguous ranges, one per CTA.  Each warp owns one or two 16-token
+//   qdecode_split_kernel  persistent, two to four CTAs of four warps per SM.  The (sequence,
+//       KV head) pairs are cut into tiles of 128 keys (192 at d = 128) and the global tile
+//       list into equal contiguous ranges, one per CTA.  Each warp owns two (three) 16-token
 //       blocks of every tile: it copies their K and V bytes into a ring of its own with
-//       bulk copies, a few tiles ahead, and keeps its own softmax state, so the warps meet only at the
-//       end of a piece, where they are merged in shared memory.  (A producer warp for the
+//       bulk copies, a few tiles ahead, and keeps its own softmax state, so the warps meet
+//       only at the end of a piece, where they are merged in shared memory.  (A producer warp for the
 //       four cost a fifth warp's registers, which the accumulators need: 128 a thread
 //       spilled, and 64 sequences of 16k-32k tokens took 432 us.)
 //         S^T = K Q^T   m16n8k16, fp16: sixteen keys by the H/G <= 8 queries.  Numbers below
@@ -58,11 +58,16 @@ constexpr float kCode = 1.f / 16777216.f;
 template <int D>
 struct QdCfg {
     static constexpr int NG = D / kQcGroup;             // scale groups
-    static constexpr int NB = 2;
+    // Blocks a warp takes at once, whose waits fill one another and which share the loads of
+    // the query fragments, and CTAs an SM holds at the registers that takes.  d = 128: three
+    // and three (4 sequences of 60k-131k tokens 47.6 us, 32 of 200-2000 20.1) rather than two
+    // and four (48.9, 23.9) or four and two (47.8, 21.7); d = 64: two and four (200 of 0-300
+    // 14.5 us) rather than four and three (15.9).
+    static constexpr int NB = D == 128 ? 3 : 2;
+    static constexpr int CTAS_PER_SM = D == 256 ? 2 : D == 128 ? 3 : 4;
     static constexpr int BT = NW * NB * kQcBlock;       // keys per tile
     static constexpr int BLOCK_BYTES = 10 * D;          // one 16-token block
     static constexpr int STAGE_BYTES = 2 * NB * BLOCK_BYTES;  // a warp's K and V blocks
-    static constexpr int CTAS_PER_SM = D == 256 ? 2 : 4;
     static constexpr int MAX_STAGES = 8;                // per warp
     static constexpr int OROW = D + 4;                  // floats per row of the merge buffer (banks)
     // shared memory: the warps' rings (NW * stages), then
@@ -956,7 +961,9 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
 }  // namespace
 
 size_t qcache_decode_workspace(int B, int H, int G, int d, int n_sms) {
-    const int per_sm = d == 256 ? QdCfg<256>::CTAS_PER_SM : QdCfg<64>::CTAS_PER_SM;
+    const int per_sm = d == 256   ? QdCfg<256>::CTAS_PER_SM
+                       : d == 128 ? QdCfg<128>::CTAS_PER_SM
+                                  : QdCfg<64>::CTAS_PER_SM;
     const int r = H / G;
     return ((size_t)per_sm * n_sms + (size_t)B * G) * (size_t)state_floats(r, d) * sizeof(float);
 }
