@@ -61,8 +61,8 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {
 // the reciprocal that turns a distance from the centre into codes.  The halves keep
 // hi - lo finite over the whole fp32 range; a scale below the smallest normal float stores
 // the group as its centre.  The reciprocal is one Newton step r (2 - s r) on the hardware
-// approximation, which for the 8-bit significands of bf16 is 1 / s rounded to nearest (the
-// tests compare every bf16 number).
+// approximation, which for the 8-bit significands of bf16 is 1 / s rounded to nearest (a
+// test puts numbers half way between codes for every significand and 201 exponents).
 struct QcGroup {
     uint32_t bits;
     float centre, inv;

@@ -529,3 +529,242 @@ def test_a_prompt_then_steps():
     for got, y in ((ko, want), (vo, allv.double().numpy())):
         assert np.linalg.norm(got.double().cpu().numpy() - y) <= 0.12 * np.linalg.norm(y)
     assert ko.shape == allk.shape and gattn_get_device_status() == 0
+
+
+def written_values(v, page=16, before=0):
+    """V rows [T,G,d] written to a fresh cache after `before` tokens and read back in fp32 (fp64 on the CPU)."""
+    T, G, d = v.shape
+    cache, table = make_pool([before + T], G, page, d, 1)
+    cu = i32([0, T])
+    w = torch.ones(d, dtype=v.dtype, device=DEV)
+    gattn_qcache_write(v.to(DEV), v.to(DEV), cache, table, i32([before + T]), w, cu, rotary_dim=0, rope_base=1e4)
+    out = gattn_qcache_read(cache, table, i32([before]), cu, total=T, dtype=torch.float32)[1]
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    return out.double().cpu().numpy()
+
+
+def test_every_scale_rounds_ties_by_its_exact_reciprocal():
+    """Groups whose scale is each normal bf16 s of 2^-100 .. 2^100, and whose numbers lie half way
+    between two codes: which way one goes shows the last bit of 1 / s.  Extremes -7.5 s and 7.5 s
+    give the step s (1 + 2^-24 at most) and the centre s / 2, both exact."""
+    s = (1 + torch.arange(128, dtype=torch.float64) / 128)[None] * 2.0 ** torch.arange(-100, 101, dtype=torch.float64)[:, None]
+    k = torch.arange(32) % 14 - 7.0
+    x = (0.5 + k + 0.5)[None] * s.reshape(-1, 1)
+    x[:, 0], x[:, 1] = -7.5 * s.reshape(-1), 7.5 * s.reshape(-1)
+    x = x.float()
+    n, sc, c = ref.encode(x.numpy())
+    assert (sc.reshape(-1) == s.reshape(-1).numpy()).all()
+    pad = -x.shape[0] % 8
+    got = written_values(torch.cat([x, x[:pad]]).reshape(-1, 1, 256)).reshape(-1, 32)[:x.shape[0]]
+    assert (got == (c + sc * n).astype(np.float32)).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_codes_clamped_where_the_centre_is_coarse(d, dt):
+    """A spread that is small against the values: the centre's rounding pushes codes past both ends."""
+    g = torch.Generator().manual_seed(d)
+    far = torch.tensor([1000.0, -333.0, 77.0, 5.0])[torch.arange(24) % 4][:, None, None]
+    v = (far + 0.02 * torch.rand(24, 2, d, generator=g) * far.abs()).to(dt)
+    n, s, c = ref.encode(v.float().numpy())
+    want = (np.repeat(c, 32, -1) + np.repeat(s, 32, -1) * n).astype(np.float32)
+    assert (np.abs(n) >= 7).any()
+    assert (written_values(v, before=5) == want).all()
+
+
+@pytest.mark.parametrize("r", range(1, 9))
+@pytest.mark.parametrize("d,rd", [(64, 48), (128, 16), (256, 112)])
+def test_decode_every_ratio_of_heads(r, d, rd):
+    case = (2 * r, 2, d, rd, 1e5, 48, [191, 1, 193, 385, 47])
+    x = decode_inputs(*case, seed=r)
+    out = run_decode(x, d, rd, 1e5)
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    assert_close(out, expected(x, case[-1], rd, 1e5), str(case))
+
+
+@pytest.mark.parametrize("d,page", [(128, 16), (128, 48), (128, 4096), (64, 80), (256, 1024)])
+def test_decode_lengths_around_tiles_and_pages(d, page):
+    """Every length around the ends of a warp's blocks and of a tile, in pages that end inside both."""
+    lens = [*range(15, 19), *range(31, 34), *range(47, 50), *range(95, 98), *range(127, 130), *range(191, 194),
+            *range(255, 258), 383, 384, 385, 577]
+    x = decode_inputs(4, 2, d, 32, 1e4, page, lens, seed=page)
+    out = run_decode(x, d, 32, 1e4)
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    assert_close(out, expected(x, lens, 32, 1e4), f"{d} {page}")
+
+
+@pytest.mark.parametrize("scale", [1e-20, 1e30])
+def test_decode_of_small_and_large_values(scale):
+    """V of far magnitudes: fp32 sums and bf16 operands carry them alike."""
+    H, G, d, page, lens = 4, 2, 128, 32, [40, 300]
+    x = decode_inputs(H, G, d, 64, 1e4, page, lens, seed=31)
+    g = torch.Generator().manual_seed(32)
+    k = torch.randn(sum(lens), G, d, generator=g).to(torch.bfloat16)
+    v = (scale * torch.randn(sum(lens), G, d, generator=g)).to(torch.bfloat16)
+    cu = i32([0, lens[0], sum(lens)])
+    gattn_qcache_write(k.to(DEV), v.to(DEV), x["cache"], x["table"], x["seqlens"], x["kw"].to(DEV), cu, rotary_dim=64,
+                       rope_base=1e4)
+    out = run_decode(x, d, 64, 1e4)
+    torch.cuda.synchronize()
+    want = expected(x, lens, 64, 1e4)
+    assert_close((out.float() / scale).to(torch.bfloat16), want / scale, f"{scale}")
+
+
+def test_the_largest_batch_mostly_unused():
+    """2048 rows of which a few hold tokens: the others get the gate of an empty sum."""
+    H, G, d, page = 2, 1, 64, 16
+    lens = [0] * 2048
+    for b, n in ((0, 3), (7, 40), (1000, 17), (1023, 200), (1024, 1), (2047, 65)):
+        lens[b] = n
+    x = decode_inputs(H, G, d, 32, 1e4, page, lens, seed=41)
+    out = run_decode(x, d, 32, 1e4)
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    assert_close(out, expected(x, lens, 32, 1e4), "2048 rows")
+    assert (out[[b for b in range(2048) if not lens[b]]] == 0).all()
+
+
+def test_every_row_unused():
+    x = decode_inputs(8, 2, 128, 64, 1e6, 32, [4, 4], seed=2)
+    x["seqlens"].zero_()
+    before = x["cache"].clone()
+    k = torch.ones(2, 2, 128, dtype=torch.bfloat16, device=DEV)
+    out = run_decode(x, 128, 64, 1e6, k_new=k, v_new=k, knorm_w=x["kw"].to(DEV))
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    assert (out == 0).all() and torch.equal(before, x["cache"])
+
+
+@pytest.mark.parametrize("case", [(64, 1, 16, torch.bfloat16, 1, 3), (128, 8, 32, torch.bfloat16, 3, 700),
+                                  (256, 5, 64, torch.float32, 2, 900), (64, 3, 48, torch.float32, 40, 31),
+                                  (256, 2, 64, torch.bfloat16, 2, 9001), (128, 1, 16, torch.bfloat16, 1, 40000)], ids=str)
+def test_write_of_many_sizes(case):
+    """Short calls, whose heads are spread, and long ones, of several passes a warp, in a padded
+    batch: V exactly, K against its exact values, padding and other rows untouched."""
+    d, G, page, dt, B, n = case
+    g = torch.Generator().manual_seed(n)
+    new = [n] + [int(torch.randint(0, 40, (1,), generator=g)) for _ in range(B - 1)]
+    before = [int(torch.randint(0, 100, (1,), generator=g)) for _ in range(B)]
+    T, reach = sum(new), [a + b for a, b in zip(new, before)]
+    cache, table = make_pool(reach, G, page, d, n)
+    kv = torch.randn(T + 5, G, 2, d, generator=g).to(dt).to(DEV)  # five rows of padding, heads strided
+    kw = (1 + 0.1 * torch.randn(d, generator=g)).to(dt)
+    cu = i32(np.concatenate([[0], np.cumsum(new)]).tolist())
+    gattn_qcache_write(kv[:, :, 0], kv[:, :, 1], cache, table, i32(reach), kw.to(DEV), cu, rotary_dim=d // 2, rope_base=1e6)
+    ko, vo = gattn_qcache_read(cache, table, i32(before), cu, total=T, dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    m, s, c = ref.encode(kv[:T, :, 1].float().cpu().numpy())
+    want = (np.repeat(c, 32, -1) + np.repeat(s, 32, -1) * m).astype(np.float32)
+    assert (vo.cpu().numpy() == want).all()
+    pos = np.concatenate([np.arange(a, b) for a, b in zip(before, reach)])
+    K = ref.norm_rope(kv[:T, :, 0].double().cpu().numpy(), kw.double().numpy(), pos, d // 2, 1e6)
+    grp = K.reshape(T, G, -1, 32)
+    step = np.repeat((grp.max(-1) - grp.min(-1)) / 15, 32, -1)
+    # half a step, the scale's rounding over 8 steps and the centre's at the group's largest, fp32 on top
+    bound = (0.5 + 8 * 2.0 ** -8) * step + (2.0 ** -8 + 2.0 ** -18) * np.repeat(np.abs(grp).max(-1), 32, -1)
+    assert (np.abs(ko.double().cpu().numpy() - K) <= bound).all()
+    used = {int(table[b, i]) for b in range(B) for i in range(-(-reach[b] // page))}
+    spare = [i for i in range(cache.shape[1]) if i not in used]
+    assert (cache[:, spare] == 255).all()
+
+
+def test_work_queued_without_waiting():
+    """Kernels that make the inputs, the operators, and kernels that use the outputs, queued one
+    behind the other: nothing starts before what it reads is there."""
+    H, G, d, rd, base, page, B, steps = 8, 2, 128, 64, 1e6, 16, 3, 20
+    g = torch.Generator().manual_seed(51)
+    start = [100, 1, 47]
+    k, v = (torch.randn(steps, B, G, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    qg = torch.randn(steps, B, H, 2 * d, generator=g).to(torch.bfloat16).to(DEV)
+    kw, qw = (torch.ones(d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+
+    def run(wait):
+        x = decode_inputs(H, G, d, rd, base, page, [n + steps for n in start], seed=52)
+        lens, pages, got = i32(start), x["table"] - 1, []
+        for s in range(steps):
+            lens = lens + 1
+            table = pages + 1
+            if s % 3 == 2:  # written and then attended, in two calls
+                gattn_qcache_write(k[s] * 0.5, v[s] * 2, x["cache"], table, lens, kw, rotary_dim=rd, rope_base=base)
+                new = {}
+            else:
+                new = dict(k_new=k[s] * 0.5, v_new=v[s] * 2, knorm_w=kw)
+            if wait:
+                torch.cuda.synchronize()
+            o = gattn_decode_qcache(qg[s, ..., :d] * 1, x["cache"], table, lens, qg[s, ..., d:] * 1, qw, rotary_dim=rd,
+                                    rope_base=base, **new)
+            if wait:
+                torch.cuda.synchronize()
+            ko, vo = gattn_qcache_read(x["cache"], table, lens - 1)
+            if wait:
+                torch.cuda.synchronize()
+            got += [o + 0, ko + 0, vo + 0]
+        torch.cuda.synchronize()
+        assert gattn_get_device_status() == 0
+        return got + [x["cache"]]
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
+
+
+def test_two_graphs_and_an_eager_call_between():
+    """Two captured steps, each with its own workspace, replayed in turn with an eager one between."""
+    cases = [(8, 2, 256, 64, 1e7, 64, [3000, 40]), (16, 8, 128, 128, 1e6, 16, [900, 901, 17])]
+    xs = [decode_inputs(*c, seed=i + 60) for i, c in enumerate(cases)]
+    on_gpu = [(x["qg"].to(DEV), x["qw"].to(DEV)) for x in xs]
+
+    def call(i, **kw):
+        c, x, (qg, qw) = cases[i], xs[i], on_gpu[i]
+        return gattn_decode_qcache(qg[..., :c[2]], x["cache"], x["table"], x["seqlens"], qg[..., c[2]:], qw,
+                                   rotary_dim=c[3], rope_base=c[4], **kw)
+
+    plain = [call(0), call(1)]
+    graphs, outs = [], []
+    for i, c in enumerate(cases):
+        need = gattn_decode_qcache_workspace_size(len(c[-1]), c[0], c[1], c[2], xs[i]["table"].shape[1] * c[5])
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            outs.append(call(i, workspace=ws))
+    for _ in range(3):
+        outs[0].zero_(), outs[1].zero_()
+        graphs[0].replay()
+        between = call(1)
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], plain[0]) and torch.equal(outs[1], plain[1]) and torch.equal(between, plain[1])
+
+
+def test_another_stream_allocates_and_two_threads():
+    """Writes and reads on a stream of the caller's, their outputs made there; then two threads at once."""
+    import threading
+
+    d, G, page, T = 128, 2, 32, 500
+    cache, table = make_pool([T], G, page, d, 70)
+    kv = torch.randn(2, T, G, d, generator=torch.Generator().manual_seed(71)).to(torch.bfloat16).to(DEV)
+    w, lens, cu = torch.ones(d, dtype=torch.bfloat16, device=DEV), i32([T]), i32([0, T])
+    torch.cuda.synchronize()
+
+    def once(stream, out):
+        for _ in range(20):
+            mine = torch.empty_like(cache)
+            gattn_qcache_write(kv[0], kv[1], mine, table, lens, w, cu, rotary_dim=64, rope_base=1e6, stream=stream)
+            out.append(gattn_qcache_read(mine, table, None, cu, total=T, stream=stream))
+            stream.synchronize()
+
+    results = [[], []]
+    streams = [torch.cuda.Stream() for _ in results]
+    once(streams[0], results[0])
+    threads = [threading.Thread(target=once, args=a) for a in zip(streams, results)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0 and [len(r) for r in results] == [40, 20]
+    for k, v in results[0] + results[1]:
+        assert torch.equal(k, results[0][0][0]) and torch.equal(v, results[0][0][1])

@@ -151,3 +151,52 @@ def test_decode_wrapper_refuses(change):
     a.update(change)
     with pytest.raises(ValueError):
         ga.gattn_decode_qcache(**a, rotary_dim=32, rope_base=1e4)
+
+
+class AnyStream:
+    cuda_stream = 0
+
+
+def calls():
+    """Each wrapper with arguments that only lack a GPU."""
+    c = args()
+    one = {**args(T=3), "cu_seqlens": None}
+    yield lambda **kw: ga.gattn_qcache_write(**{**c, "rotary_dim": 32, "rope_base": 1e4, **kw})
+    yield lambda **kw: ga.gattn_qcache_write(**{**one, "rotary_dim": 32, "rope_base": 1e4, **kw})
+    yield lambda **kw: ga.gattn_qcache_read(**{**dict(qcache=c["qcache"], block_table=c["block_table"]), **kw})
+    yield lambda **kw: ga.gattn_decode_qcache(**{**dict(
+        q_new=torch.zeros(3, 4, 64, dtype=torch.bfloat16), qcache=c["qcache"], block_table=c["block_table"],
+        seqlens=c["seqlens"], gate=torch.zeros(3, 4, 64, dtype=torch.bfloat16),
+        qnorm_w=torch.ones(64, dtype=torch.bfloat16), rotary_dim=32, rope_base=1e4), **kw})
+
+
+def test_wrappers_refuse_host_tensors_and_things_that_are_none():
+    for call in calls():
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(stream=AnyStream())
+        for bad in (None, 3, [1, 2]):
+            with pytest.raises(ValueError, match="must be a tensor"):
+                call(block_table=bad)
+
+
+def test_wrappers_refuse_options_of_other_types_and_sizes():
+    write_packed, write_one, read, decode = calls()
+    for call in (write_packed, write_one, decode):
+        with pytest.raises(ValueError):
+            call(rotary_dim=1 << 40)
+        with pytest.raises((TypeError, OverflowError)):
+            call(rotary_dim=1 << 90)
+        with pytest.raises(TypeError):
+            call(rotary_dim="32")
+        with pytest.raises(TypeError):
+            call(rope_base="1e4")
+    with pytest.raises(ValueError):
+        read(cu_seqlens=torch.zeros(4, dtype=torch.int32), stream=AnyStream())  # how many rows?
+    with pytest.raises(ValueError):
+        read(cu_seqlens=torch.zeros(4, dtype=torch.int32), total=1 << 40)
+    with pytest.raises(ValueError):
+        read(cu_seqlens=torch.zeros(4, dtype=torch.int32), total=-1)
+    with pytest.raises(ValueError):
+        decode(workspace=torch.zeros(64, 2, dtype=torch.uint8)[:, 0])
