@@ -229,7 +229,6 @@ struct WriteShared {
     // lives on warps per SM (with 16 of them it moved 2.9 TB/s, whatever the instructions).
     float4 factors[kWarps / TEAM][8][34];
     float4 plain[8][34];  // the same of features that are not turned (the norm weights, and zeros), a token's lanes
-    float weights[256];
     uint4 rows[kWarps][kStages][2][kChunks];  // K and V as copied, ahead of their use
 };
 
@@ -298,7 +297,6 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     for (int i = threadIdx.x; i < 4 * 34; i += 32 * kWarps) sh.plain[4][i] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int e = threadIdx.x; e < D; e += 32 * kWarps) {
         const float w = to_float(static_cast<const T*>(p.knorm_w)[e]);
-        sh.weights[e] = w;
         reinterpret_cast<float*>(sh.plain)[place(e, 0)] = w;
     }
     Place mine;  // of token t0 + lane
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     for (int pass = 0; pass < passes; ++pass) {
         for (int i0 = 0; i0 < half; i0 += 32) {
             const int i = min(i0 + lane, half - 1);
-            const float wl = sh.weights[i], wh = sh.weights[i + half];
+            const float wl = reinterpret_cast<const float*>(sh.plain)[place(i, 0)], wh = reinterpret_cast<const float*>(sh.plain)[place(i + half, 0)];
             float* const lo = factors + place(i, 0);
             float* const hi = factors + place(i + half, 0);
             for (int k = mate_id; k < TPW; k += TEAM) {
