@@ -76,8 +76,7 @@ struct QdCfg {
     static constexpr int OFF_QSUM = OFF_CINIT + NG * 64;     // bf16 [2][8 heads][8 groups], high and low parts
     static constexpr int OFF_QSC = OFF_QSUM + 256;           // float [8] logit scale of a head
     static constexpr int OFF_ML = OFF_QSC + 32;              // float [NW][8][2] the warps' (max, sum)
-    static constexpr int OFF_TOT = OFF_ML + NW * 64;         // float [8][2] the merged (max, sum)
-    static constexpr int OFF_BAR = OFF_TOT + 64;             // mbarrier [NW][MAX_STAGES]
+    static constexpr int OFF_BAR = OFF_ML + NW * 64;         // mbarrier [NW][MAX_STAGES]
     static constexpr int OFF_MISC = OFF_BAR + NW * 8 * MAX_STAGES;
     static constexpr int OFF_RED = OFF_MISC + 16;            // int [NW][2] scan scratch
     static constexpr int OFF_OBUF = OFF_RED + 32;            // float [r][OROW]; the sine table (rd/2 float2) before it
@@ -168,24 +167,27 @@ __device__ void scan_batch(const int32_t* seqlens, int first_len, int B, int Lma
     }
 }
 
-// How many tiles lie ahead of unit u.
-__device__ __forceinline__ int tiles_ahead(int u, const Sequences& q, int B, int G) {
+// Tile i of the nt of KV head g of sequence b.
+struct TileAt {
+    int b, g, i, nt;
+};
+// The first tile at or behind unit u, and how many lie ahead of it.
+__device__ __forceinline__ TileAt first_tile(int u, const Sequences& q, int B, int G, int& ahead) {
     int lo = 0, hi = B - 1;  // largest b with G * units(b) <= u
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (G * (q.tiles[mid] + kPieceTiles * q.live[mid]) <= u) lo = mid; else hi = mid - 1;
     }
-    const int nt = q.tiles[lo + 1] - q.tiles[lo];
+    TileAt t;
+    t.b = lo;
+    t.nt = q.tiles[lo + 1] - q.tiles[lo];
     const int rel = u - G * (q.tiles[lo] + kPieceTiles * q.live[lo]);
-    if (nt == 0) return G * q.tiles[lo];  // past the last piece
-    const int g = (int)((unsigned)rel / (unsigned)(nt + kPieceTiles)), i = rel - g * (nt + kPieceTiles) - kPieceTiles;
-    return G * q.tiles[lo] + g * nt + max(i, 0);
+    t.g = (int)((unsigned)rel / (unsigned)(t.nt + kPieceTiles));
+    t.i = max(rel - t.g * (t.nt + kPieceTiles) - kPieceTiles, 0);
+    ahead = G * q.tiles[lo] + (t.nt ? t.g * t.nt + t.i : 0);  // nt = 0: past the last piece
+    return t;
 }
-
-// Tile x of the batch: sequence b, KV head g, tile i of its nt.
-struct TileAt {
-    int b, g, i, nt;
-};
+// Tile x of the batch.
 __device__ __forceinline__ TileAt tile_at(int x, const Sequences& q, int B, int G) {
     int lo = 0, hi = B - 1;  // largest b with G * tiles[b] <= x
     while (lo < hi) {
@@ -415,13 +417,12 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 
     const WorkSplit split(p.G * (seqs.tiles[p.B] + kPieceTiles * seqs.live[p.B]), gridDim.x);
     if ((int)blockIdx.x >= split.N) return;
-    // this CTA's tiles: x0 .. x0 + n_tiles - 1 of the batch
-    int x0 = 0, n_tiles = 0;
-    {
-        const int x = tiles_ahead(split.start(blockIdx.x + (lane & 1)), seqs, p.B, p.G);
-        x0 = __shfl_sync(0xffffffffu, x, 0);
-        n_tiles = __shfl_sync(0xffffffffu, x, 1) - x0;
-    }
+    // this CTA's tiles: x0 .. x0 + n_tiles - 1 of the batch; `at` is the first of the piece at hand
+    int x;
+    TileAt at = first_tile(split.start(blockIdx.x + (lane & 1)), seqs, p.B, p.G, x);
+    const int x0 = __shfl_sync(0xffffffffu, x, 0), n_tiles = __shfl_sync(0xffffffffu, x, 1) - x0;
+    at = TileAt{__shfl_sync(0xffffffffu, at.b, 0), __shfl_sync(0xffffffffu, at.g, 0), __shfl_sync(0xffffffffu, at.i, 0),
+                __shfl_sync(0xffffffffu, at.nt, 0)};
     const int64_t plane = (int64_t)p.num_pages * p.G * (p.page_size / kQcBlock) * C::BLOCK_BYTES;
     const int bpp = p.page_size / kQcBlock;
     // ---- the warp's copies run n_stages tiles ahead.  Lane j holds the addresses of the
@@ -430,8 +431,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     // phase, so the stages' parities flip together.
     int sent = 0;
     uint64_t src[C::NB] = {};
-    TileAt at = {};  // first the CTA's first tile, then the piece at hand
-    uint4 qraw = {}, wraw = {};  // its queries and their norm weights as loaded
+    uint4 qraw = {}, wraw = {};  // the piece's queries and their norm weights as loaded
     auto load_queries = [&]() {
         qraw = load_first_query<D>(p, at.b, at.g);
         wraw = reinterpret_cast<const uint4*>(p.qnorm_w)[threadIdx.x % QueryLanes<D>::LPH];
@@ -442,12 +442,8 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         if ((sent & 31) == 0) {
 #pragma unroll
             for (int j = 0; j < C::NB; ++j) src[j] = 0;
-            const TileAt t = tile_at(x0 + min(sent + lane, n_tiles - 1), seqs, p.B, p.G);
-            if (sent == 0) {
-                at = TileAt{__shfl_sync(0xffffffffu, t.b, 0), __shfl_sync(0xffffffffu, t.g, 0),
-                            __shfl_sync(0xffffffffu, t.i, 0), __shfl_sync(0xffffffffu, t.nt, 0)};
-                load_queries();  // ahead of the copies, behind which they would wait 2 us
-            }
+            TileAt t{at.b, at.g, at.i + sent + lane, at.nt};
+            if (sent > 0 || t.i >= at.nt) t = tile_at(x0 + min(sent + lane, n_tiles - 1), seqs, p.B, p.G);
             if (sent + lane < n_tiles) {
 #pragma unroll
                 for (int j = 0; j < C::NB; ++j) {
@@ -498,6 +494,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         }
         ++sent;
     };
+    if (n_tiles > 0) load_queries();  // ahead of the copies, behind which they would wait 2 us
     for (int s = 0; s < n_stages; ++s) send(s);
 
     const int gid = lane >> 2, t = lane & 3;
@@ -706,31 +703,94 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 
         // -------- end of the piece: merge the four warps, then finish or hand over
         float* ml = reinterpret_cast<float*>(tail + C::OFF_ML);
-        float* obuf = reinterpret_cast<float*>(tail + C::OFF_OBUF);
         if (gid == 0) reinterpret_cast<float4*>(ml)[warp * 4 + t] = make_float4(m_run[0], cacc[2], m_run[1], cacc[3]);
+        // merged maximum and sum of head h, and the weights of the warps' states
+        auto weights = [&](int h, float (&f)[NW], float& mx, float& l) {
+            float2 v[NW];
+            mx = -INFINITY;
+            l = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                v[w] = reinterpret_cast<const float2*>(ml)[w * 8 + h];
+                mx = fmaxf(mx, v[w].x);
+            }
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                f[w] = v[w].x == -INFINITY ? 0.f : ex2_approx(v[w].x - mx);
+                l += f[w] != 0.f ? f[w] * v[w].y : 0.f;
+            }
+        };
+        // features 4 gid' .. of row tile m and head 2t + e as a pair
+        auto place = [&](float* rows, int m, int e) {
+            return reinterpret_cast<float2*>(rows + (2 * t + e) * C::OROW + (m >> 1) * 32 + gid * 4 + (m & 1) * 2);
+        };
+        // the state's own pair there: rows 0-7 lower codes, 8-15 bytes, and the centres' part
+        auto own = [&](int m, int e) {
+            const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * (m >> 1) + t);
+            const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * (m >> 1) + t);
+            const float c = e ? c1 : c0;
+            return make_float2(fmaf(64.f, oacc[m][e], c), fmaf(4.f, oacc[m][2 + e] - oacc[m][e], c));
+        };
+        auto finish = [&](auto merged) {  // merged(h, e): features e .. e + 3 of head h
+            bf16* out = static_cast<bf16*>(p.out) + ((int64_t)at.b * p.H + at.g * r) * D;
+            float* ps = p.part + ((int64_t)blockIdx.x + (int64_t)at.b * p.G + at.g) * state_floats(r, D);
+            for (int j = 4 * threadIdx.x; j < r * D; j += 4 * THREADS) {
+                const int h = j / D, e = j % D;
+                float mx, l;
+                const float4 o = merged(h, e, mx, l);
+                if (alone) {
+                    l = 1.f / l;
+                    float v[4] = {o.x * l, o.y * l, o.z * l, o.w * l};
+                    gated4(p, at.b, at.g * r + h, e, v);
+                    *reinterpret_cast<uint2*>(out + j) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                } else {
+                    *reinterpret_cast<float4*>(ps + j) = o;
+                    if (e == 0) {
+                        ps[r * D + h] = mx;
+                        ps[r * D + r + h] = l;
+                    }
+                }
+            }
+        };
+        if (n >= n_tiles) {
+            // the CTA's last piece: each warp lays its state into its ring, which is done with
+            float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+            for (int m = 0; m < 2 * C::NG; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 o = own(m, e);
+                    if (2 * t + e < r) *place(mine, m, e) = o;
+                }
+            __syncthreads();
+            finish([&](int h, int e, float& mx, float& l) {
+                float f[NW];
+                weights(h, f, mx, l);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    if (f[w] == 0.f) continue;  // a warp without keys may hold anything
+                    const float4 a = *reinterpret_cast<const float4*>(smem + w * n_stages * C::STAGE_BYTES + (h * C::OROW + e) * 4);
+                    o.x = fmaf(f[w], a.x, o.x);
+                    o.y = fmaf(f[w], a.y, o.y);
+                    o.z = fmaf(f[w], a.z, o.z);
+                    o.w = fmaf(f[w], a.w, o.w);
+                }
+                return o;
+            });
+            break;
+        }
+        // the rings hold the next piece's blocks: four rounds over one buffer, in each of which
+        // the warps add to different quarters of the features, loads first
+        float* obuf = reinterpret_cast<float*>(tail + C::OFF_OBUF);
         __syncthreads();
-        // weight of this warp's state for the lane's two heads
         float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + 2 * t + e) * 2]);
-            const float mine = ml[(warp * 8 + 2 * t + e) * 2];
-            f[e] = mine == -INFINITY ? 0.f : ex2_approx(mine - mx);
+            float all[NW], mx, l;
+            weights(2 * t + e, all, mx, l);
+            f[e] = warp == 0 ? all[0] : warp == 1 ? all[1] : warp == 2 ? all[2] : all[3];
         }
-        if (threadIdx.x < 8) {  // the merged maximum and sum of head threadIdx.x
-            float mx = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, ml[(w * 8 + threadIdx.x) * 2]);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float mw = ml[(w * 8 + threadIdx.x) * 2];
-                l += mw == -INFINITY ? 0.f : ex2_approx(mw - mx) * ml[(w * 8 + threadIdx.x) * 2 + 1];
-            }
-            reinterpret_cast<float2*>(tail + C::OFF_TOT)[threadIdx.x] = make_float2(mx, l);
-        }
-        // four rounds; in each the warps add to different quarters of the features, loads first
         constexpr int MQ = C::NG / 2;  // row tiles a quarter
 #pragma unroll 1
         for (int k = 0; k < NW; ++k) {
@@ -739,57 +799,35 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
             for (int qt = 0; qt < 4; ++qt) {
                 if (qt != quarter) continue;
                 float2 o[MQ][2];
-                auto place = [&](int m, int e) {
-                    return reinterpret_cast<float2*>(obuf + (2 * t + e) * C::OROW + (m >> 1) * 32 + gid * 4 + (m & 1) * 2);
-                };
 #pragma unroll
                 for (int i = 0; i < MQ; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        o[i][e] = k && 2 * t + e < r ? *place(qt * MQ + i, e) : make_float2(0.f, 0.f);
+                        o[i][e] = k && 2 * t + e < r ? *place(obuf, qt * MQ + i, e) : make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < MQ; ++i) {
-                    const int m = qt * MQ + i;
-                    const float c0 = __shfl_sync(0xffffffffu, cacc[0], 4 * (m >> 1) + t);
-                    const float c1 = __shfl_sync(0xffffffffu, cacc[1], 4 * (m >> 1) + t);
+                for (int i = 0; i < MQ; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        const float2 a = own(qt * MQ + i, e);
                         if (f[e] != 0.f) {
-                            o[i][e].x = fmaf(f[e], fmaf(64.f, oacc[m][e], e ? c1 : c0), o[i][e].x);
-                            o[i][e].y = fmaf(f[e], fmaf(4.f, oacc[m][2 + e] - oacc[m][e], e ? c1 : c0), o[i][e].y);
+                            o[i][e].x = fmaf(f[e], a.x, o[i][e].x);
+                            o[i][e].y = fmaf(f[e], a.y, o[i][e].y);
                         }
-                        if (2 * t + e < r) *place(m, e) = o[i][e];
+                        if (2 * t + e < r) *place(obuf, qt * MQ + i, e) = o[i][e];
                     }
-                }
             }
             __syncthreads();
         }
-        const float2* tot = reinterpret_cast<const float2*>(tail + C::OFF_TOT);
-        if (alone) {
-            bf16* out = static_cast<bf16*>(p.out) + ((int64_t)at.b * p.H + at.g * r) * D;
-            for (int j = 4 * threadIdx.x; j < r * D; j += 4 * THREADS) {
-                const int h = j / D, e = j % D;
-                const float4 o = *reinterpret_cast<const float4*>(obuf + h * C::OROW + e);
-                const float l = 1.f / tot[h].y;
-                float v[4] = {o.x * l, o.y * l, o.z * l, o.w * l};
-                gated4(p, at.b, at.g * r + h, e, v);
-                *reinterpret_cast<uint2*>(out + j) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-            }
-        } else {
-            float* ps = p.part + ((int64_t)blockIdx.x + (int64_t)at.b * p.G + at.g) * state_floats(r, D);
-            for (int j = 4 * threadIdx.x; j < r * D; j += 4 * THREADS)
-                *reinterpret_cast<float4*>(ps + j) = *reinterpret_cast<const float4*>(obuf + (j / D) * C::OROW + j % D);
-            if (threadIdx.x < r) {
-                ps[r * D + threadIdx.x] = tot[threadIdx.x].x;
-                ps[r * D + r + threadIdx.x] = tot[threadIdx.x].y;
-            }
-        }
+        finish([&](int h, int e, float& mx, float& l) {
+            float all[NW];
+            weights(h, all, mx, l);
+            return *reinterpret_cast<const float4*>(obuf + h * C::OROW + e);
+        });
         // the next piece: the next KV head, or the next sequence that holds anything
         at.i = 0;
         if (++at.g == p.G) {
             at.g = 0;
-            do { ++at.b; } while (at.b < p.B && seqs.tiles[at.b + 1] == seqs.tiles[at.b]);
-            if (at.b == p.B) break;
+            do { ++at.b; } while (seqs.tiles[at.b + 1] == seqs.tiles[at.b]);  // there is one: tiles are left
             at.nt = seqs.tiles[at.b + 1] - seqs.tiles[at.b];
         }
         load_queries();
