@@ -431,6 +431,8 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     // phase, so the stages' parities flip together.
     int sent = 0;
     uint64_t src[C::NB] = {};
+    uint32_t newest = 0;  // bit j: tile x0 + 32 k + j's blocks of this warp hold the sequence's last token
+    bool cache_ready = !after_write;
     uint4 qraw = {}, wraw = {};  // the piece's queries and their norm weights as loaded
     auto load_queries = [&]() {
         qraw = load_first_query<D>(p, at.b, at.g);
@@ -444,11 +446,13 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
             for (int j = 0; j < C::NB; ++j) src[j] = 0;
             TileAt t{at.b, at.g, at.i + sent + lane, at.nt};
             if (sent > 0 || t.i >= at.nt) t = tile_at(x0 + min(sent + lane, n_tiles - 1), seqs, p.B, p.G);
+            bool last = false;
             if (sent + lane < n_tiles) {
 #pragma unroll
                 for (int j = 0; j < C::NB; ++j) {
                     const int blk = (t.i * NW + warp) * C::NB + j;
                     if (blk * kQcBlock < seqs.lens[t.b]) {
+                        last = (blk + 1) * kQcBlock >= seqs.lens[t.b];
                         const int slot = page_of(blk, p.by_page);
                         int page = p.block_table[(int64_t)t.b * p.max_pages + slot];
                         if (page < 0 || page >= p.num_pages) {
@@ -459,10 +463,14 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                     }
                 }
             }
+            newest = __ballot_sync(0xffffffffu, last);
         }
-        if (sent == 0 && after_write) {  // the appended rows are being written by the kernel before this one
+        // the appended rows are being written by the kernel ahead of this one; the blocks
+        // that hold none of them are copied meanwhile
+        if (!cache_ready && (newest >> (sent & 31) & 1u)) {
             pdl_wait_prerequisites();
             fence_proxy_async_global();
+            cache_ready = true;
         }
         uint64_t a[C::NB];
 #pragma unroll
