@@ -37,9 +37,16 @@
 //       with every nibble shifted down and or-ed into a power of two (28 instructions for 16
 //       keys of a group) 64 sequences of 16k-32k tokens, d = 256, took 181 us and 4 of
 //       60k-131k, d = 128, 55 us; with bytes and lower codes (18) 168 and 49.
+//       Measured: 64 sequences of 16k-32k tokens, 2 heads of 256 (1.08 GB), 164 us with the
+//       combine, 6.6 TB/s, 0.97 of a copy; 4 of 60k-131k, 4 of 128 (0.25 GB), 47 us, 5.4 TB/s.
+//       A cached byte takes 0.095 warp instructions at d = 256 and 0.124 at d = 128, where
+//       what a key costs whatever its length (softmax, loop, copies) is shared by half the
+//       features; with 12 warps an SM, half of the issue slots and of the ALU are taken and
+//       the rest goes into the waits between dependent instructions.  Some 8 us of every
+//       call are fixed: lengths, search, first copies, queries, merge, combine.
 //   qdecode_combine_kernel  merges the partial states of pieces that several CTAs share
 //       and applies the gate; a (sequence, KV head) that one CTA covered is finished by
-//       that CTA.
+//       that CTA.  1 to 2 us behind the split kernel, of which the loads of the states are most.
 #include <cuda_fp16.h>
 
 #include "qcache.cuh"
@@ -50,7 +57,8 @@ namespace {
 constexpr int NW = 4;  // warps, each with its own 16-token blocks of every tile
 constexpr int THREADS = 32 * NW;
 // What starting and merging a (sequence, KV head) piece costs, in tiles: the work split
-// counts it, so a CTA with many short sequences gets fewer tiles.
+// counts it, so a CTA with many short sequences gets fewer tiles (256 sequences of 100-1500
+// tokens, 4 x 128: 44.1 us with two, 45.8 with one, 45.3 with three).
 constexpr int kPieceTiles = 2;
 // What a code of one is worth as an operand of the K product: the lowest fp16 bit.
 constexpr float kCode = 1.f / 16777216.f;
@@ -997,7 +1005,8 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
     if (e != cudaSuccess) return e;
     // Eight warps share a head's states where a sequence may be spread over many CTAs, two
     // where there are about as many (sequence, KV head) pairs as CTAs and so a state or two
-    // each (200 sequences of 0-300 tokens, 4 x 3 heads: 18.0 us with two warps, 21.0 with eight).
+    // each (measured on an earlier split: 200 sequences of 0-300 tokens, 4 x 3 heads, 18.0 us
+    // with two warps, 21.0 with eight).
     const dim3 heads((unsigned)(p.B * p.H));
     if ((int64_t)p.B * p.G * 2 <= n_ctas)
         return launch_early(qdecode_combine_kernel<D, 8>, heads, dim3(256), 0, stream, p, n_ctas);

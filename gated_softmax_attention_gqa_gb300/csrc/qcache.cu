@@ -4,11 +4,15 @@
 // number and leaves 0.625, the read the reverse, so HBM bounds both as long as the
 // arithmetic stays small: at 6.8 TB/s an SM has some 14 instruction slots for a written
 // number.  So a lane takes 16 features (half a scale group) of one token and walks its KV
-// heads: the token's sines and cosines (made once per warp, in shared memory) and their
-// products with the norm weights are shared by all heads, and what a group costs
+// heads: the token's sines and cosines and their products with the norm weights (made once
+// per warp, in shared memory) are shared by all heads, and what a group costs
 // (extremes, scale, reciprocal) is shared by 32 numbers and two lanes.  The chain of
 // lookups that finds a token's row (sequence, length, page) is walked by one lane per
 // token for all the tokens a warp will deal with.
+//
+// Measured, 131072 tokens of 2 heads of 256 in bf16 (353 MB each way): the read 54 us,
+// 6.5 TB/s, which is HBM; the write 82 us, 4.3 TB/s, held by instruction issue (two thirds
+// of the slots are taken; 15 instructions a number of K and V).
 #include "qcache.cuh"
 
 namespace gattn {
@@ -225,8 +229,8 @@ struct WriteShared {
     // What K' = (x wc + partner ws) / rms takes, products of the norm weights with cosine
     // and sine (the rotation's sign in ws): quads of wc in rows 0-3, of ws in rows 4-7, a
     // float4 a lane in Vec16 order.  The spare two spread a token's features, 32 at a time,
-    // over the banks.  In shared memory rather than in registers, because the kernel
-    // lives on warps per SM (with 16 of them it moved 2.9 TB/s, whatever the instructions).
+    // over the banks.  In shared memory rather than in 32 registers, which are worth a CTA
+    // per SM (131072 tokens, 2 x 256: five hold 87 us, four 92; six spill, 94).
     float4 factors[kWarps / TEAM][8][34];
     float4 plain[8][34];  // the same of features that are not turned (the norm weights, and zeros), a token's lanes
     uint4 rows[kWarps][kStages][2][kChunks];  // K and V as copied, ahead of their use
@@ -235,7 +239,8 @@ struct WriteShared {
 // A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass.  `TEAM` of the block's
 // warps (one or all) take the same tokens, `passes` passes of them, and every TEAM-th of the
 // heads [blockIdx.y heads, ...); they make the factors together.  A warp's rows are copied to
-// shared memory two heads ahead.
+// shared memory two heads ahead (with loads straight to registers the warps waited for HBM a
+// third of the time: 101 us for 131072 tokens of 2 x 256, 87 with the copies).
 template <int D, typename T, int TEAM>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
     qcache_write_kernel(const __grid_constant__ QcacheWriteParams p, int passes, int heads) {
@@ -461,8 +466,10 @@ __global__ void __launch_bounds__(32 * kWarps)
 // How a call is cut: passes a warp takes (their lookups go together), KV heads of a block,
 // warps that share a token's heads.  A call too small to fill the device with one warp for
 // all heads of its tokens takes one pass and spreads the heads, over a block's warps first.
-// (Passes of a long call: the write of 131072 tokens, 2 x 256, takes 106 us with two and 101
-// with four; the read of 211k tokens, 4 x 128, 107 with two and 119 with four.)
+// Passes of a long call: the write of 131072 tokens, 2 x 256, takes 92 us with two, 87 with
+// four, 86 with eight; the read of 211k tokens, 4 x 128, 107 with two and 119 with four.
+// A read has no factors to share between heads and is spread twice as far: 8k tokens of
+// 8 x 128 take 8.1 us rather than 9.2, but their write 17.1 rather than 14.5.
 struct Cut {
     int passes, heads, team;
     dim3 grid;

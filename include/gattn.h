@@ -368,6 +368,7 @@ gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, cons
  * each; starts [B] int32 device array, NULL: zeros).  Rows at or past cu_seqlens[B], and
  * those of a sequence whose range leaves [0, Lmax) (GATTN_DEVICE_BAD_SEQLEN) or whose
  * page is not in the pool (GATTN_DEVICE_BAD_PAGE), are left as they were.
+ * T = 0 returns GATTN_OK without launching anything; T * G <= 2^30.
  */
 gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, int num_pages, int page_size,
                                int max_pages, const int32_t* starts, const int32_t* cu_seqlens, int T, int B, int G,
@@ -387,7 +388,11 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
  *          GATTN_DEVICE_BAD_SEQLEN and leaves that row of out unwritten.
  * k_new, v_new, knorm_w  NULL for no append, else [B,G,d] contiguous and [d] bf16: the
  *          new token is first written to the cache, as by gattn_qcache_write.
- * H/G <= 8, B <= 2048; only GATTN_BF16 (implied).
+ * H/G <= 8, B <= 2048, B * G * (Lmax / 64 + 8) < 2^31 (others: GATTN_ERR_UNSUPPORTED);
+ * only GATTN_BF16 (implied).  Sums are fp32 and weights reach 2^8 before they are
+ * normalised: V of magnitudes up to 1e30 is exact to rounding, from about 1e33 on a long
+ * sequence's sum may overflow.
+ * A sequence's blocks that do not hold its newest token may be read while the append runs.
  * workspace  >= gattn_decode_qcache_workspace_size(B, H, G, d, Lmax) bytes, 256-byte
  *          aligned; out [B,H*d] bf16, 16-byte aligned.
  */
