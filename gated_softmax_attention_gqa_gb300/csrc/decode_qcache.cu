@@ -409,7 +409,13 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + C::OFF_MISC);
     // After a write of the appended rows everything but the cache is ready: that kernel
     // lets this one start only once those ahead of it have finished.
-    if (!after_write) pdl_wait_prerequisites();
+    bool cache_ready = !after_write;
+    auto wait_for_cache = [&]() {
+        pdl_wait_prerequisites();
+        fence_proxy_async_global();  // plain stores of the kernel ahead, bulk copies here
+        cache_ready = true;
+    };
+    if (cache_ready) wait_for_cache();
     pdl_launch_dependents();  // the combine kernel may become resident; it waits for this grid to finish
     const int first_len = (int)threadIdx.x < p.B ? p.seqlens[threadIdx.x] : 0;
 
@@ -424,7 +430,10 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     scan_batch<D>(p.seqlens, first_len, p.B, Lmax, seqs, reinterpret_cast<int*>(tail + C::OFF_RED));  // ends with a block barrier
 
     const WorkSplit split(p.G * (seqs.tiles[p.B] + kPieceTiles * seqs.live[p.B]), gridDim.x);
-    if ((int)blockIdx.x >= split.N) return;
+    if ((int)blockIdx.x >= split.N) {
+        if (!cache_ready) wait_for_cache();  // this grid's end means the end of the one ahead
+        return;
+    }
     // this CTA's tiles: x0 .. x0 + n_tiles - 1 of the batch; `at` is the first of the piece at hand
     int x;
     TileAt at = first_tile(split.start(blockIdx.x + (lane & 1)), seqs, p.B, p.G, x);
@@ -440,7 +449,6 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
     int sent = 0;
     uint64_t src[C::NB] = {};
     uint32_t newest = 0;  // bit j: tile x0 + 32 k + j's blocks of this warp hold the sequence's last token
-    bool cache_ready = !after_write;
     uint4 qraw = {}, wraw = {};  // the piece's queries and their norm weights as loaded
     auto load_queries = [&]() {
         qraw = load_first_query<D>(p, at.b, at.g);
@@ -475,11 +483,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         }
         // the appended rows are being written by the kernel ahead of this one; the blocks
         // that hold none of them are copied meanwhile
-        if (!cache_ready && (newest >> (sent & 31) & 1u)) {
-            pdl_wait_prerequisites();
-            fence_proxy_async_global();
-            cache_ready = true;
-        }
+        if (!cache_ready && (newest >> (sent & 31) & 1u)) wait_for_cache();
         uint64_t a[C::NB];
 #pragma unroll
         for (int j = 0; j < C::NB; ++j) a[j] = __shfl_sync(0xffffffffu, src[j], sent & 31);
@@ -848,6 +852,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         }
         load_queries();
     }
+    if (!cache_ready) wait_for_cache();
     // every copy that was sent lands before the block leaves (none is left unless a wait ran out)
     for (; done < sent; ++done) mbar_wait_drain(bars + 8 * (done % n_stages), (uint32_t)(done / n_stages) & 1u, p.status);
 }

@@ -494,8 +494,10 @@ cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) 
                        : (c.team > 1 ? qcache_write_kernel<D, bf16, kWarps> : qcache_write_kernel<D, bf16, 1>);
     const size_t shared = fp32 ? (c.team > 1 ? sizeof(WriteShared<float, kWarps>) : sizeof(WriteShared<float, 1>))
                                : (c.team > 1 ? sizeof(WriteShared<bf16, kWarps>) : sizeof(WriteShared<bf16, 1>));
-    const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), 227 * 1024);
-    if (e != cudaSuccess) return e;
+    if (shared > 48 * 1024) {
+        const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), (int)shared);
+        if (e != cudaSuccess) return e;
+    }
     return launch_early(kernel, c.grid, dim3(32 * kWarps), shared, stream, p, c.passes, c.heads);
 }
 

@@ -768,3 +768,61 @@ def test_another_stream_allocates_and_two_threads():
     assert gattn_get_device_status() == 0 and [len(r) for r in results] == [40, 20]
     for k, v in results[0] + results[1]:
         assert torch.equal(k, results[0][0][0]) and torch.equal(v, results[0][0][1])
+
+
+def test_captured_behind_copies_fills_and_joins():
+    """Operators whose captured predecessor is no kernel (a copy, a fill) or two (a join)."""
+    H, G, d, rd, base, page, lens = 8, 2, 128, 64, 1e6, 32, [70, 33]
+    x = decode_inputs(H, G, d, rd, base, page, lens, seed=81)
+    g = torch.Generator().manual_seed(82)
+    k, v = (torch.randn(2, G, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    qg, qw, kw = x["qg"].to(DEV), x["qw"].to(DEV), x["kw"].to(DEV)
+    want_cache = x["cache"].clone()
+    gattn_qcache_write(k, v, want_cache, x["table"], x["seqlens"], kw, rotary_dim=rd, rope_base=base)
+    want = gattn_decode_qcache(qg[..., :d], want_cache, x["table"], x["seqlens"], qg[..., d:], qw, rotary_dim=rd, rope_base=base)
+    want_rows = gattn_qcache_read(want_cache, x["table"], x["seqlens"] - 1)
+    torch.cuda.synchronize()
+    kc, vc, lens_c, cache = torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(x["seqlens"]), torch.zeros_like(x["cache"])
+    starts, junk = x["seqlens"] - 1, torch.empty(1 << 20, device=DEV)
+    ws = torch.empty(gattn_decode_qcache_workspace_size(2, H, G, d, x["table"].shape[1] * page), dtype=torch.uint8, device=DEV)
+    other = torch.cuda.Stream()
+
+    def ahead(how):
+        if how == "copy":
+            lens_c.copy_(x["seqlens"])
+        elif how == "fill":
+            junk.zero_()
+        else:
+            other.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(other):
+                junk.mul_(0)
+            torch.cuda.current_stream().wait_stream(other)
+
+    def run(how, append):
+        cache.copy_(x["cache"])
+        kc.copy_(k), vc.copy_(v)
+        new = dict(k_new=kc, v_new=vc, knorm_w=kw) if append else {}
+        if not append:
+            lens_c.copy_(x["seqlens"])
+            ahead(how)
+            gattn_qcache_write(kc, vc, cache, x["table"], lens_c, kw, rotary_dim=rd, rope_base=base)
+        lens_c.copy_(x["seqlens"])
+        ahead(how)
+        out = gattn_decode_qcache(qg[..., :d], cache, x["table"], lens_c, qg[..., d:], qw, rotary_dim=rd, rope_base=base,
+                                  workspace=ws, **new)
+        ahead(how)
+        return (out, *gattn_qcache_read(cache, x["table"], starts))
+
+    for how in ("copy", "fill", "join"):
+        for append in (False, True):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = run(how, append)
+            for _ in range(2):
+                lens_c.zero_(), cache.zero_(), kc.zero_()
+                graph.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(got[0], want), (how, append)
+                assert all(torch.equal(a, b) for a, b in zip(got[1:], want_rows)), (how, append)
+                assert torch.equal(cache, want_cache)
+    assert gattn_get_device_status() == 0
