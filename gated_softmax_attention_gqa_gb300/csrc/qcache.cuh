@@ -87,7 +87,7 @@ constexpr float kQcMagic = 12582912.f;
 // of the nearest quarter turn, at most pi/4, goes through the Taylor series of sine and
 // cosine (first terms left out: a^11/11! < 2e-9, a^12/12! < 2e-10).
 __device__ __forceinline__ void rope_turn_sincos(uint64_t f, int pos, float* s, float* c) {
-    const uint32_t t = (uint32_t)(((uint64_t)(int64_t)pos * f) >> 32);  // 2^-32 turns
+    const uint32_t t = __umulhi((uint32_t)pos, (uint32_t)f) + (uint32_t)pos * (uint32_t)(f >> 32);  // 2^-32 turns
     const uint32_t q = (t + 0x20000000u) >> 30;                         // nearest quarter turn
     const float a = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
     const float a2 = a * a;
