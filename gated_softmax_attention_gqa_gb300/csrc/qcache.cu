@@ -11,8 +11,8 @@
 // token for all the tokens a warp will deal with.
 //
 // Measured, 131072 tokens of 2 heads of 256 in bf16 (353 MB each way): the read 54 us,
-// 6.5 TB/s, which is HBM; the write 82 us, 4.3 TB/s, held by instruction issue (two thirds
-// of the slots are taken; 15 instructions a number of K and V).
+// 6.5 TB/s, which is HBM; the write 76 us, 4.6 TB/s, held by instruction issue (two thirds
+// of the slots are taken).
 #include "qcache.cuh"
 
 namespace gattn {
@@ -237,7 +237,7 @@ struct WriteShared {
 };
 
 // A token is spread over D / 16 lanes, 32 / (D / 16) tokens to a pass.  `TEAM` of the block's
-// warps (one or all) take the same tokens, `passes` passes of them, and every TEAM-th of the
+// warps take the same tokens, `passes` passes of them (one, if they are several), and every TEAM-th of the
 // heads [blockIdx.y heads, ...); they make the factors together.  A warp's rows are copied to
 // shared memory two heads ahead (with loads straight to registers the warps waited for HBM a
 // third of the time: 101 us for 131072 tokens of 2 x 256, 87 with the copies).
@@ -473,67 +473,77 @@ __global__ void __launch_bounds__(32 * kWarps)
     }
 }
 
-// How a call is cut: passes a warp takes (their lookups go together), KV heads of a block,
-// warps that share a token's heads.  A call too small to fill the device with one warp for
-// all heads of its tokens takes one pass and spreads the heads, over a block's warps first.
-// Passes of a long call: the write of 131072 tokens, 2 x 256, takes 92 us with two, 87 with
-// four, 86 with eight; the read of 211k tokens, 4 x 128, 107 with two and 119 with four.
-// A read has no factors to share between heads and is spread twice as far: 8k tokens of
-// 8 x 128 take 8.1 us rather than 9.2, but their write 17.1 rather than 14.5.
+// How a call is cut: passes a warp takes (their lookups and a lane's frequency go together),
+// KV heads of a block, warps that share a token's heads.  A call too small to fill the device
+// with one warp for all heads of its tokens spreads the heads, over a block's warps first.
+// Passes of a write: their set-up weighs the more the fewer heads follow it, and as they
+// grow the warps get few.  131072 tokens of 2 x 256 take 92 us with two, 87 with four, 86
+// with eight; 40000 30.5, 27.0, 26.2 and 28.7 with one, two, four and eight, 12000 10.5, 9.5,
+// 11.1, 16.3; 32000 of 8 x 128 36.0, 36.9, 40.8, 52.3.
+// A read's: 211k tokens of 4 x 128 107 us with two, 119 with four.  A read has no factors to
+// share between heads and is spread twice as far: 8k tokens of 8 x 128 take 8.1 us rather
+// than 9.2, but their write 17.1 rather than 14.5.
 struct Cut {
     int passes, heads, team;
     dim3 grid;
 };
 template <int D>
-Cut cut_of(int T, int G, int passes, int spread) {
+Cut cut_of(int T, int G, bool read) {
     constexpr int TPW = 32 / (D / 16);
     const int64_t want = 8 * (int64_t)device_sm_count(), groups = ((int64_t)T + TPW - 1) / TPW;
-    Cut c{passes, G, 1, dim3()};
-    if (groups < passes * want) c.passes = 1;
-    if (G > 1 && groups < want) c.team = kWarps;
-    while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < spread * want) c.heads = (c.heads + 1) / 2;
+    Cut c{1, G, 1, dim3()};
+    if (read) {
+        if (groups >= 2 * want) c.passes = 2;
+    } else {
+        while (2 * c.passes * G <= 8 && groups >= 3 * (int64_t)c.passes * c.passes * want) c.passes *= 2;
+    }
+    if (G > 1 && groups < want) c.team = G > 2 ? kWarps : 2;
+    while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < (read ? 2 : 1) * want) c.heads = (c.heads + 1) / 2;
     const int tokens = kWarps / c.team * TPW * c.passes;
     c.grid = dim3((unsigned)((T + tokens - 1) / tokens), (unsigned)((G + c.heads - 1) / c.heads));
     return c;
 }
 
-template <int D>
-cudaError_t write_d(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G, 4, 1);
-    auto kernel = fp32 ? (c.team > 1 ? qcache_write_kernel<D, float, kWarps> : qcache_write_kernel<D, float, 1>)
-                       : (c.team > 1 ? qcache_write_kernel<D, bf16, kWarps> : qcache_write_kernel<D, bf16, 1>);
-    const size_t shared = fp32 ? (c.team > 1 ? sizeof(WriteShared<float, kWarps>) : sizeof(WriteShared<float, 1>))
-                               : (c.team > 1 ? sizeof(WriteShared<bf16, kWarps>) : sizeof(WriteShared<bf16, 1>));
+template <int D, typename T, int TEAM>
+cudaError_t write_team(const QcacheWriteParams& p, const Cut& c, cudaStream_t stream) {
+    const auto kernel = qcache_write_kernel<D, T, TEAM>;
+    constexpr int shared = (int)sizeof(WriteShared<T, TEAM>);
     if (shared > 48 * 1024) {
-        const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), (int)shared);
+        const cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kernel), shared);
         if (e != cudaSuccess) return e;
     }
     return launch_early(kernel, c.grid, dim3(32 * kWarps), shared, stream, p, c.passes, c.heads);
 }
+template <int D, typename T>
+cudaError_t write_d(const QcacheWriteParams& p, cudaStream_t stream) {
+    const Cut c = cut_of<D>(p.T, p.G, false);
+    return c.team == 1 ? write_team<D, T, 1>(p, c, stream)
+         : c.team == 2 ? write_team<D, T, 2>(p, c, stream)
+                       : write_team<D, T, kWarps>(p, c, stream);
+}
 
-template <int D>
-cudaError_t read_d(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G, 2, 2);
-    auto kernel = fp32 ? qcache_read_kernel<D, float> : qcache_read_kernel<D, bf16>;
-    return launch_early(kernel, c.grid, dim3(32 * kWarps), 0, stream, p, c.passes, c.heads, c.team);
+template <int D, typename T>
+cudaError_t read_d(const QcacheReadParams& p, cudaStream_t stream) {
+    const Cut c = cut_of<D>(p.T, p.G, true);
+    return launch_early(qcache_read_kernel<D, T>, c.grid, dim3(32 * kWarps), 0, stream, p, c.passes, c.heads, c.team);
 }
 
 }  // namespace
 
 cudaError_t launch_qcache_write(const QcacheWriteParams& p, bool fp32, cudaStream_t stream) {
     switch (p.d) {
-        case 64: return write_d<64>(p, fp32, stream);
-        case 128: return write_d<128>(p, fp32, stream);
-        case 256: return write_d<256>(p, fp32, stream);
+        case 64: return fp32 ? write_d<64, float>(p, stream) : write_d<64, bf16>(p, stream);
+        case 128: return fp32 ? write_d<128, float>(p, stream) : write_d<128, bf16>(p, stream);
+        case 256: return fp32 ? write_d<256, float>(p, stream) : write_d<256, bf16>(p, stream);
         default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_qcache_read(const QcacheReadParams& p, bool fp32, cudaStream_t stream) {
     switch (p.d) {
-        case 64: return read_d<64>(p, fp32, stream);
-        case 128: return read_d<128>(p, fp32, stream);
-        case 256: return read_d<256>(p, fp32, stream);
+        case 64: return fp32 ? read_d<64, float>(p, stream) : read_d<64, bf16>(p, stream);
+        case 128: return fp32 ? read_d<128, float>(p, stream) : read_d<128, bf16>(p, stream);
+        case 256: return fp32 ? read_d<256, float>(p, stream) : read_d<256, bf16>(p, stream);
         default: return cudaErrorInvalidValue;
     }
 }
