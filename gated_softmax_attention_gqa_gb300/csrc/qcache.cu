@@ -480,20 +480,22 @@ __global__ void __launch_bounds__(32 * kWarps)
 // grow the warps get few.  131072 tokens of 2 x 256 take 92 us with two, 87 with four, 86
 // with eight; 40000 30.5, 27.0, 26.2 and 28.7 with one, two, four and eight, 12000 10.5, 9.5,
 // 11.1, 16.3; 32000 of 8 x 128 36.0, 36.9, 40.8, 52.3.
-// A read's: 211k tokens of 4 x 128 107 us with two, 119 with four.  A read has no factors to
-// share between heads and is spread twice as far: 8k tokens of 8 x 128 take 8.1 us rather
-// than 9.2, but their write 17.1 rather than 14.5.
+// A read has little set-up and one pass is best (211k tokens of 4 x 128 86.6 us, 88.4 with two,
+// 97.5 with four; in fp32 150.8, 158.0, 177.4), but for long calls whose rows are long to read and
+// short to write (131072 tokens of 2 x 256 in bf16: 57.8 with one, 54.0 with two).  It has no
+// factors to share between heads and is spread twice as far: 8k tokens of 8 x 128 take 8.1 us
+// rather than 9.2, but their write 17.1 rather than 14.5.
 struct Cut {
     int passes, heads, team;
     dim3 grid;
 };
-template <int D>
+template <int D, typename E>
 Cut cut_of(int T, int G, bool read) {
     constexpr int TPW = 32 / (D / 16);
     const int64_t want = 8 * (int64_t)device_sm_count(), groups = ((int64_t)T + TPW - 1) / TPW;
     Cut c{1, G, 1, dim3()};
     if (read) {
-        if (groups >= 2 * want) c.passes = 2;
+        if (D == 256 && sizeof(E) == 2 && groups >= 8 * want) c.passes = 2;
     } else {
         while (2 * c.passes * G <= 8 && groups >= 3 * (int64_t)c.passes * c.passes * want) c.passes *= 2;
     }
@@ -516,7 +518,7 @@ cudaError_t write_team(const QcacheWriteParams& p, const Cut& c, cudaStream_t st
 }
 template <int D, typename T>
 cudaError_t write_d(const QcacheWriteParams& p, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G, false);
+    const Cut c = cut_of<D, T>(p.T, p.G, false);
     return c.team == 1 ? write_team<D, T, 1>(p, c, stream)
          : c.team == 2 ? write_team<D, T, 2>(p, c, stream)
                        : write_team<D, T, kWarps>(p, c, stream);
@@ -524,7 +526,7 @@ cudaError_t write_d(const QcacheWriteParams& p, cudaStream_t stream) {
 
 template <int D, typename T>
 cudaError_t read_d(const QcacheReadParams& p, cudaStream_t stream) {
-    const Cut c = cut_of<D>(p.T, p.G, true);
+    const Cut c = cut_of<D, T>(p.T, p.G, true);
     return launch_early(qcache_read_kernel<D, T>, c.grid, dim3(32 * kWarps), 0, stream, p, c.passes, c.heads, c.team);
 }
 
