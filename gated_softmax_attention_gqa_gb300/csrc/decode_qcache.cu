@@ -37,8 +37,8 @@
 //       with every nibble shifted down and or-ed into a power of two (28 instructions for 16
 //       keys of a group) 64 sequences of 16k-32k tokens, d = 256, took 181 us and 4 of
 //       60k-131k, d = 128, 55 us; with bytes and lower codes (18) 168 and 49.
-//       Measured: 64 sequences of 16k-32k tokens, 2 heads of 256 (1.08 GB), 164 us with the
-//       combine, 6.6 TB/s, 0.97 of a copy; 4 of 60k-131k, 4 of 128 (0.25 GB), 47 us, 5.4 TB/s.
+//       Measured: 64 sequences of 16k-32k tokens, 2 heads of 256 (1.08 GB), 166 us with the
+//       combine, 6.5 TB/s, 0.96 of a copy; 4 of 60k-131k, 4 of 128 (0.25 GB), 47 us, 5.4 TB/s.
 //       A cached byte takes 0.095 warp instructions at d = 256 and 0.124 at d = 128, where
 //       what a key costs whatever its length (softmax, loop, copies) is shared by half the
 //       features; with 12 warps an SM, half of the issue slots and of the ALU are taken and
