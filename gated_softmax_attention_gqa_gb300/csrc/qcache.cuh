@@ -26,11 +26,6 @@ constexpr int kQcGroup = 32;  // features per scale
 
 __host__ __device__ __forceinline__ int64_t qc_block_bytes(int d) { return 10 * (int64_t)d; }
 
-// Byte offset of a block inside one plane.
-__device__ __forceinline__ int64_t qc_block_offset(int page, int g, int slot, int G, int page_size, int d) {
-    return (((int64_t)page * G + g) * (page_size / kQcBlock) + slot / kQcBlock) * qc_block_bytes(d);
-}
-
 __device__ __forceinline__ int page_of(int x, const PageDiv& d) {
     return d.mul ? (int)(__umulhi((uint32_t)x, d.mul) >> d.shift) : x;
 }

@@ -826,3 +826,28 @@ def test_captured_behind_copies_fills_and_joins():
                 assert all(torch.equal(a, b) for a, b in zip(got[1:], want_rows)), (how, append)
                 assert torch.equal(cache, want_cache)
     assert gattn_get_device_status() == 0
+
+
+def test_read_returns_ordinary_tensors():
+    """The two results of a read: contiguous, apart from each other, kept, cloned and changed on their own."""
+    d, G, T = 64, 3, 37
+    cache, table = make_pool([T], G, 16, d, 90)
+    kv = torch.randn(2, T, G, d, generator=torch.Generator().manual_seed(91)).to(torch.bfloat16).to(DEV)
+    cu = i32([0, T])
+    gattn_qcache_write(kv[0], kv[1], cache, table, i32([T]), torch.ones(d, dtype=torch.bfloat16, device=DEV), cu,
+                       rotary_dim=32, rope_base=1e4)
+    for dt in (torch.bfloat16, torch.float32):
+        k, v = gattn_qcache_read(cache, table, None, cu, total=T, dtype=dt)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        gattn_qcache_read(cache, table, None, cu, k_out=ko, v_out=vo)
+        assert k.shape == v.shape == (T, G, d) and k.dtype == v.dtype == dt and k.is_contiguous() and v.is_contiguous()
+        assert torch.equal(k, ko) and torch.equal(v, vo)
+        k.zero_()
+        assert torch.equal(v, vo) and torch.equal(v.transpose(0, 1).clone(), vo.transpose(0, 1))
+        del k
+        v += 1
+        assert torch.equal(v, vo + 1)
+        with torch.inference_mode():
+            assert torch.equal(gattn_qcache_read(cache, table, None, cu, total=T, dtype=dt)[1], vo)
+    none = gattn_qcache_read(cache, table, None, i32([0, 0]), total=0)
+    assert none[0].shape == none[1].shape == (0, G, d)
