@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "qcache_internal.h"
 
 using namespace gattn;
 

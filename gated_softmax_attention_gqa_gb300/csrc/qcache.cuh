@@ -17,7 +17,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "internal.h"
+#include "qcache_internal.h"
 
 namespace gattn {
 

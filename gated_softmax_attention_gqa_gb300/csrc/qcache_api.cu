@@ -4,7 +4,6 @@
 #include <cstdint>
 #include <cstring>
 
-#include "internal.h"
 #include "qcache.cuh"
 
 using namespace gattn;
