@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 5 : 4)
         const float w = to_float(static_cast<const T*>(p.knorm_w)[e]);
         reinterpret_cast<float*>(sh.plain)[place(e, 0)] = w;
     }
-    Place mine;  // of token t0 + lane
+    Place mine;  // of token t0 + lane: passes * TPW <= 32 (cut_of)
     const bool ok = report(lane < passes * TPW ? place_new(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
 
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int lc = lane % LPR, e0 = first_feature(lc) - (8 - RUN) * (lc & 1);
     const int g0 = blockIdx.y * heads + warp % team, g1 = min(p.G, (int)(blockIdx.y + 1) * heads);
     if (t0 >= p.T || g0 >= g1) return;
-    Place mine;  // of token t0 + lane
+    Place mine;  // of token t0 + lane: passes * TPW <= 32 (cut_of)
     const bool ok = report(lane < passes * TPW ? place_cached(p, t0 + lane, mine) : kSkip, p.status);
     if (!ok) mine = Place{0, -1, 0};
     const int64_t head = (int64_t)(p.page_size / kQcBlock) * qc_block_bytes(D), plane = (int64_t)p.num_pages * p.G * head;
@@ -494,10 +494,14 @@ Cut cut_of(int T, int G, bool read) {
     constexpr int TPW = 32 / (D / 16);
     const int64_t want = 8 * (int64_t)device_sm_count(), groups = ((int64_t)T + TPW - 1) / TPW;
     Cut c{1, G, 1, dim3()};
+    // A warp's tokens are looked up by one lane each, so it takes 32 at most: four passes at
+    // head_dim 64.
+    constexpr int kMostPasses = 32 / TPW;
     if (read) {
         if (D == 256 && sizeof(E) == 2 && groups >= 8 * want) c.passes = 2;
     } else {
-        while (2 * c.passes * G <= 8 && groups >= 3 * (int64_t)c.passes * c.passes * want) c.passes *= 2;
+        while (2 * c.passes <= kMostPasses && 2 * c.passes * G <= 8 && groups >= 3 * (int64_t)c.passes * c.passes * want)
+            c.passes *= 2;
     }
     if (G > 1 && groups < want) c.team = G > 2 ? kWarps : 2;
     while (c.heads > c.team && groups * c.team * ((G + c.heads - 1) / c.heads) < (read ? 2 : 1) * want) c.heads = (c.heads + 1) / 2;
