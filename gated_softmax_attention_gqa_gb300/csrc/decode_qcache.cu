@@ -726,7 +726,10 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         // -------- end of the piece: merge the four warps, then finish or hand over
         float* ml = reinterpret_cast<float*>(tail + C::OFF_ML);
         if (gid == 0) reinterpret_cast<float4*>(ml)[warp * 4 + t] = make_float4(m_run[0], cacc[2], m_run[1], cacc[3]);
-        // merged maximum and sum of head h, and the weights of the warps' states
+        // Merged maximum and sum of head h, and the weights of the warps' states.  A weight of zero
+        // multiplies its state like any other: the maximum passes over NaN logits (a warp that met
+        // only such has -infinity, as one without keys, whose state is zeros), so that a NaN
+        // reaches the output through the sums wherever its key lies in the work split.
         auto weights = [&](int h, float (&f)[NW], float& mx, float& l) {
             float2 v[NW];
             mx = -INFINITY;
@@ -739,7 +742,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 f[w] = v[w].x == -INFINITY ? 0.f : ex2_approx(v[w].x - mx);
-                l += f[w] != 0.f ? f[w] * v[w].y : 0.f;
+                l += f[w] * v[w].y;
             }
         };
         // features 4 gid' .. of row tile m and head 2t + e as a pair
@@ -791,7 +794,6 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    if (f[w] == 0.f) continue;  // a warp without keys may hold anything
                     const float4 a = *reinterpret_cast<const float4*>(smem + w * n_stages * C::STAGE_BYTES + (h * C::OROW + e) * 4);
                     o.x = fmaf(f[w], a.x, o.x);
                     o.y = fmaf(f[w], a.y, o.y);
@@ -831,10 +833,8 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float2 a = own(qt * MQ + i, e);
-                        if (f[e] != 0.f) {
-                            o[i][e].x = fmaf(f[e], a.x, o[i][e].x);
-                            o[i][e].y = fmaf(f[e], a.y, o[i][e].y);
-                        }
+                        o[i][e].x = fmaf(f[e], a.x, o[i][e].x);
+                        o[i][e].y = fmaf(f[e], a.y, o[i][e].y);
                         if (2 * t + e < r) *place(obuf, qt * MQ + i, e) = o[i][e];
                     }
             }
@@ -861,7 +861,8 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
 
 // Merge the partial states of one (sequence, query head) that several CTAs share and
 // apply the gate: warp w of NWC sums every NWC-th state, lane l owning D / 32 features, and
-// the warps meet in shared memory.  A sequence of length 0 gets the gate of an empty sum.
+// the warps meet in shared memory.  States of weight zero take part (their NaN do).  A
+// sequence of length 0 gets the gate of an empty sum.
 template <int D, int NWC>
 __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_constant__ QcacheDecodeParams p, int n_ctas) {
     constexpr int DPL = D / 32, VEC = DPL < 4 ? DPL : 4, CH = NWC == 8 ? 8 : 4, EPT = (D + 32 * NWC - 1) / (32 * NWC);
@@ -956,7 +957,6 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
             const float w = ms[j] == -INFINITY ? 0.f : ex2_approx(ms[j] - mx);
-            if (w == 0.f) continue;
             den = fmaf(w, ls[j], den);
 #pragma unroll
             for (int k = 0; k < DPL; ++k) num[k] = fmaf(w, os[j][k], num[k]);
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
 #pragma unroll
     for (int w = 0; w < NWC; ++w) {
         f[w] = sm[w][0] == -INFINITY ? 0.f : ex2_approx(sm[w][0] - mx);
-        l += f[w] != 0.f ? f[w] * sm[w][1] : 0.f;
+        l += f[w] * sm[w][1];
     }
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {
@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(32 * NWC) qdecode_combine_kernel(const __grid_
         if (e >= D) break;
         float o = 0.f;
 #pragma unroll
-        for (int w = 0; w < NWC; ++w) o += f[w] != 0.f ? f[w] * so[w][e] : 0.f;
+        for (int w = 0; w < NWC; ++w) o += f[w] * so[w][e];
         out[e] = __float2bfloat16_rn(gate_apply(p.gate_mode, z[k], o / l));
     }
 }

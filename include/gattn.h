@@ -392,6 +392,8 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
  * only GATTN_BF16 (implied).  Sums are fp32 and weights reach 2^8 before they are
  * normalised: V of magnitudes up to 1e30 is exact to rounding, from about 1e33 on a long
  * sequence's sum may overflow.
+ * A NaN in a live token's K makes its KV head's outputs of that sequence NaN, one in its V
+ * those of the group's features, whatever the token's weight; rows past seqlens may hold anything.
  * A sequence's blocks that do not hold its newest token may be read while the append runs.
  * workspace  >= gattn_decode_qcache_workspace_size(B, H, G, d, Lmax) bytes, 256-byte
  *          aligned; out [B,H*d] bf16, 16-byte aligned.
