@@ -50,16 +50,6 @@ unsigned int* status_ptr() {
     return ptrs[dev];
 }
 
-int sm_count() {
-    static int cached[64] = {};
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64 && cached[dev] > 0) return cached[dev];
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev >= 0 && dev < 64) cached[dev] = n;
-    return n;
-}
-
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

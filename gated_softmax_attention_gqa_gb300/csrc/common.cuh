@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "device_once.h"
 #include "gattn.h"
 
 namespace gattn {
@@ -209,27 +210,6 @@ __device__ __forceinline__ void scale8_bf16(const float (&x)[8], const float (&w
         const float2 v = mul2(mul2(make_float2(x[e], x[e + 1]), make_float2(w[e], w[e + 1])), r2);
         o[e >> 1] = pack_bf16x2(v.x, v.y);
     }
-}
-
-// Raise a kernel's dynamic shared-memory limit once per device (host side).
-// `func` identifies the kernel; up to 16 kernels per device are remembered
-// (beyond that the attribute is simply set again on every call).
-inline cudaError_t set_smem_once(const void* func, int bytes) {
-    static const void* seen[64][16] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64)
-        for (int i = 0; i < 16; ++i)
-            if (seen[dev][i] == func) return cudaSuccess;
-    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess || dev < 0 || dev >= 64) return e;
-    for (int i = 0; i < 16; ++i)
-        if (!seen[dev][i]) {
-            seen[dev][i] = func;
-            break;
-        }
-    return cudaSuccess;
 }
 
 // ------------------------------------------------------------------ mbarrier
