@@ -43,14 +43,18 @@ PageDiv page_div(int d) {
     return PageDiv{(uint32_t)((((uint64_t)1 << (31 + k)) / (uint64_t)d) + 1), (uint32_t)(k - 1)};
 }
 
+constexpr int kMostTokens = INT32_MAX - 1024;  // of a sequence: the kernels round lengths up to tiles in 31 bits
+
+bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
 // The pool's geometry: what every entry point checks of it.
 gattn_status check_pool(const void* cache, const int32_t* table, int num_pages, int page_size, int max_pages, int B,
                         int G, int d) {
     if (!cache || !table || num_pages < 1 || page_size < 1 || max_pages < 1 || B < 1 || G < 1 || d < 1)
         return GATTN_ERR_INVALID_ARG;
     if (!aligned(cache, 16) || !aligned(table, 4)) return GATTN_ERR_INVALID_ARG;
-    if (!(d == 64 || d == 128 || d == 256) || page_size % kQcBlock != 0) return GATTN_ERR_UNSUPPORTED;
-    if ((int64_t)max_pages * page_size > INT32_MAX - 1024) return GATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(d) || page_size % kQcBlock != 0) return GATTN_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page_size > kMostTokens) return GATTN_ERR_INVALID_ARG;
     return GATTN_OK;
 }
 
@@ -59,6 +63,13 @@ gattn_status check_rope(int d, int rotary_dim, double rope_base, float eps) {
     if (rotary_dim > 0 && !(rope_base > 0.0 && std::isfinite(rope_base))) return GATTN_ERR_INVALID_ARG;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return GATTN_ERR_INVALID_ARG;
     return rotary_dim % 16 ? GATTN_ERR_UNSUPPORTED : GATTN_OK;
+}
+
+// The batches a decode step takes, of heads, dimensions and lengths that are right otherwise.
+bool batch_ok(int B, int H, int G, int64_t Lmax) {
+    if (H / G > 8 || B > decode_max_batch()) return false;
+    // the kernels count the batch's 64-key tiles (and a few per head and sequence) in 31 bits
+    return (int64_t)B * G * (Lmax / 64 + 8) <= INT32_MAX;
 }
 
 // Rows are moved 16 bytes at a time.
@@ -124,7 +135,7 @@ gattn_status write_tokens(const void* k, const void* v, void* qcache, const int3
 extern "C" {
 
 size_t gattn_qcache_bytes(int num_pages, int G, int page_size, int d) {
-    if (num_pages < 1 || G < 1 || page_size < kQcBlock || page_size % kQcBlock || d < 64 || d % 64) return 0;
+    if (num_pages < 1 || G < 1 || page_size < kQcBlock || page_size % kQcBlock || !head_dim_ok(d)) return 0;
     return (size_t)2 * num_pages * G * (page_size / kQcBlock) * (size_t)qc_block_bytes(d);
 }
 
@@ -172,7 +183,8 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
 }
 
 size_t gattn_decode_qcache_workspace_size(int B, int H, int G, int d, int Lmax) {
-    if (B < 1 || H < 1 || G < 1 || d < 1 || Lmax < 1 || H % G != 0) return 0;
+    if (B < 1 || H < 1 || G < 1 || H % G != 0 || !head_dim_ok(d) || Lmax < 1 || Lmax > kMostTokens) return 0;
+    if (!batch_ok(B, H, G, Lmax)) return 0;
     const int n = device_sm_count();
     return n > 0 ? round_up(qcache_decode_workspace(B, H, G, d, n), 256) : 0;
 }
@@ -191,9 +203,7 @@ gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const voi
     gattn_status st = check_pool(qcache, block_table, num_pages, page_size, max_pages, B, G, d);
     if (st != GATTN_OK) return st;
     if ((st = check_rope(d, rotary_dim, rope_base, eps)) != GATTN_OK) return st;
-    if (H / G > 8 || B > decode_max_batch()) return GATTN_ERR_UNSUPPORTED;
-    // the kernels count the batch's 64-key tiles (and a few per head and sequence) in 31 bits
-    if ((int64_t)B * G * ((int64_t)max_pages * page_size / 64 + 8) > INT32_MAX) return GATTN_ERR_UNSUPPORTED;
+    if (!batch_ok(B, H, G, (int64_t)max_pages * page_size)) return GATTN_ERR_UNSUPPORTED;
     if (!aligned(seqlens, 4) || !aligned(out, 16)) return GATTN_ERR_INVALID_ARG;
     const bool append = k_new || v_new;
     if (append && (!k_new || !v_new || !knorm_w)) return GATTN_ERR_INVALID_ARG;

@@ -332,7 +332,7 @@ gattn_status gattn_decode_noalloc(const void* q_new, const void* kv_cache, const
  * Nothing of a page needs to be initialised before tokens are written to it.  Two live
  * tokens must not share a cache row (two sequences naming one page write different
  * rows of it, or only read it); calls that write and read the same rows are ordered by
- * their streams.
+ * their streams.  gattn_qcache_bytes is 0 for a geometry that is not supported.
  */
 size_t gattn_qcache_bytes(int num_pages, int G, int page_size, int d);
 
@@ -396,7 +396,8 @@ gattn_status gattn_qcache_read(const void* qcache, const int32_t* block_table, i
  * those of the group's features, whatever the token's weight; rows past seqlens may hold anything.
  * A sequence's blocks that do not hold its newest token may be read while the append runs.
  * workspace  >= gattn_decode_qcache_workspace_size(B, H, G, d, Lmax) bytes, 256-byte
- *          aligned; out [B,H*d] bf16, 16-byte aligned.
+ *          aligned (the size is 0 for what the call refuses); out [B,H*d] bf16, 16-byte
+ *          aligned.
  */
 size_t gattn_decode_qcache_workspace_size(int B, int H, int G, int d, int Lmax);
 gattn_status gattn_decode_qcache(const void* q_new, const void* k_new, const void* v_new, void* qcache,
