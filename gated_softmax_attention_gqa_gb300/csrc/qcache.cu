@@ -185,11 +185,12 @@ __device__ __forceinline__ void encode_store(const Vec16 (&x)[2], float rinv, fl
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         q[n] = n ? qc_group(lo[n], hi[n]) : qc_group(lo[n] * rinv, hi[n] * rinv);
-        inside = inside && fabsf(q[n].centre) <= 112.f * bf16_lo(q[n].bits);
         if (n == 0) {
             q[n].centre *= rms;
             q[n].inv *= rinv;
         }
+        // false, too, where rinv took the reciprocal past fp32's range (steps below 3e-39 rinv)
+        inside = inside && fabsf(q[n].centre) * q[n].inv <= 112.f;
     }
     uint32_t w[2][2];
     if (__all_sync(0xffffffffu, inside)) {
@@ -199,11 +200,16 @@ __device__ __forceinline__ void encode_store(const Vec16 (&x)[2], float rinv, fl
             w[n][1] = encode8<false>(x[n].p + 4, q[n]);
         }
     } else {
+        Vec16 k = x[0];
+        if (!(q[0].inv < INFINITY)) {  // K in its group's measure
+            q[0] = qc_group(lo[0] * rinv, hi[0] * rinv);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            w[n][0] = encode8<true>(x[n].p, q[n]);
-            w[n][1] = encode8<true>(x[n].p + 4, q[n]);
+            for (int i = 0; i < 8; ++i) k.p[i] = mul2(k.p[i], both(rinv));
         }
+        w[0][0] = encode8<true>(k.p, q[0]);
+        w[0][1] = encode8<true>(k.p + 4, q[0]);
+        w[1][0] = encode8<true>(x[1].p, q[1]);
+        w[1][1] = encode8<true>(x[1].p + 4, q[1]);
     }
     // lanes j and j ^ 2 of a slab hold the same features of its two groups, which meet in the
     // words of both runs; the first group's lane stores the words of run 0, the other run 1's

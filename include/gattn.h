@@ -352,6 +352,8 @@ size_t gattn_qcache_bytes(int num_pages, int G, int page_size, int d);
  * seqlens    [B] int32 device array: tokens in each sequence AFTER the write.  The n new
  *            ones take positions seqlens[b]-n .. seqlens[b]-1.  A length above Lmax or
  *            below n sets GATTN_DEVICE_BAD_SEQLEN and that sequence is left alone.
+ * Norms are sums of squares in fp32: numbers of K up to 1e17, and down to 1e-38 with eps
+ * 1e-6, keep the format's accuracy.
  * T = 0 returns GATTN_OK without launching anything; T * G <= 2^30.
  */
 gattn_status gattn_qcache_write(const void* k, const void* v, void* qcache, const int32_t* block_table, int num_pages,
