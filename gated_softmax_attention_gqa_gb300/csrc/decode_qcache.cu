@@ -416,6 +416,7 @@ __global__ void __launch_bounds__(THREADS, QdCfg<D>::CTAS_PER_SM)
         cache_ready = true;
     };
     if (cache_ready) wait_for_cache();
+    else fence_proxy_async_global();  // the rows of earlier calls were plain stores too
     pdl_launch_dependents();  // the combine kernel may become resident; it waits for this grid to finish
     const int first_len = (int)threadIdx.x < p.B ? p.seqlens[threadIdx.x] : 0;
 
