@@ -388,8 +388,9 @@ def gattn_qcache_read(qcache, block_table, starts=None, cu_seqlens=None, *, tota
     Rows cu_seqlens[b] .. cu_seqlens[b+1]-1 receive the tokens starts[b], starts[b]+1, ... of
     sequence b; both are int32 on the device.  cu_seqlens None: one token per sequence
     (total = B); starts None: from token 0.  total is the number of rows, cu_seqlens[B] or
-    more (rows past it are left as they were).  k_out, v_out: contiguous tensors to fill;
-    without them the two are the halves of one [2,total,G,d] allocation."""
+    more (rows past it are left as they were).  k_out, v_out: contiguous tensors to fill,
+    in their own dtype (`dtype` is then not looked at); without them the two are the halves of one
+    [2,total,G,d] allocation."""
     if dtype not in DTYPES:
         raise ValueError("dtype must be bfloat16 or float32")
     st, k, v = _lib.qcache().read(qcache, block_table, starts, cu_seqlens, total, DTYPES[dtype], k_out, v_out,

@@ -33,17 +33,19 @@
 //             scales multiply P instead (they are per key and group), and the centres' part,
 //             sum_k p_k centre_k, is one product for all groups, in whose spare rows ones
 //             sum the weights.
-//       What the unpacking costs the ALU, which is the pipe that holds d = 128 back, decides:
+//       What the unpacking costs the ALU decides:
 //       with every nibble shifted down and or-ed into a power of two (28 instructions for 16
 //       keys of a group) 64 sequences of 16k-32k tokens, d = 256, took 181 us and 4 of
 //       60k-131k, d = 128, 55 us; with bytes and lower codes (18) 168 and 49.
 //       Measured: 64 sequences of 16k-32k tokens, 2 heads of 256 (1.08 GB), 166 us with the
 //       combine, 6.5 TB/s, 0.96 of a copy; 4 of 60k-131k, 4 of 128 (0.25 GB), 47 us, 5.4 TB/s.
-//       A cached byte takes 0.095 warp instructions at d = 256 and 0.124 at d = 128, where
-//       what a key costs whatever its length (softmax, loop, copies) is shared by half the
-//       features; with 12 warps an SM, half of the issue slots and of the ALU are taken and
-//       the rest goes into the waits between dependent instructions.  Some 8 us of every
-//       call are fixed: lengths, search, first copies, queries, merge, combine.
+//       Of that 8 to 13 us are the call's own (lengths, search, first copies, queries, merge,
+//       combine, and the more pieces the more); what lies above goes at the rate of a copy at
+//       d = 256 and d = 128: 4 of 65536, 131072 and 262144 tokens, 4 heads of 128, take 34.6,
+//       58.4 and 106.5 us, their bytes 24.7, 49.5 and 98.9.  At d = 64, where what a key costs
+//       whatever its length (softmax, loop, copies) is shared by half the features again, instructions
+//       hold it at 0.75 of a copy: 32 of 16384, 32768 and 65536, 8 heads, take 79.6, 146.4 and
+//       279.2 us, their bytes 49.5, 99.0 and 197.9.
 //   qdecode_combine_kernel  merges the partial states of pieces that several CTAs share
 //       and applies the gate; a (sequence, KV head) that one CTA covered is finished by
 //       that CTA.  1 to 2 us behind the split kernel, of which the loads of the states are most.
@@ -57,8 +59,9 @@ namespace {
 constexpr int NW = 4;  // warps, each with its own 16-token blocks of every tile
 constexpr int THREADS = 32 * NW;
 // What starting and merging a (sequence, KV head) piece costs, in tiles: the work split
-// counts it, so a CTA with many short sequences gets fewer tiles (256 sequences of 100-1500
-// tokens, 4 x 128: 44.1 us with two, 45.8 with one, 45.3 with three).
+// counts it, so a CTA with many short sequences gets fewer tiles.  us with one, two and three:
+// 256 sequences of 100-1500 tokens, 4 x 128, 45.9, 42.4, 42.5; 48 of 1-4096, 8 x 128, 37.5, 33.4,
+// 34.8; 32 of 200-2000, 8 x 128, 19.8, 19.3, 20.3; 32 of 200-3000, 4 x 256, 24.1, 23.7, 22.7.
 constexpr int kPieceTiles = 2;
 // What a code of one is worth as an operand of the K product: the lowest fp16 bit.
 constexpr float kCode = 1.f / 16777216.f;
@@ -1015,8 +1018,11 @@ cudaError_t launch_d(const QcacheDecodeParams& p, bool after_write, cudaStream_t
     if (e != cudaSuccess) return e;
     // Eight warps share a head's states where a sequence may be spread over many CTAs, two
     // where there are about as many (sequence, KV head) pairs as CTAs and so a state or two
-    // each (measured on an earlier split: 200 sequences of 0-300 tokens, 4 x 3 heads, 18.0 us
-    // with two warps, 21.0 with eight).
+    // each.  us with two and eight: one sequence of 32768 tokens, 2 x 256, 32.3, 15.6; one of 131072,
+    // 4 x 128, 30.4, 23.6; 8 of 8192, 2 x 256, 17.1, 15.9; 200 of 0-300, 4 x 64, 13.8, 18.9; 32 of
+    // 200-2000, 8 x 128, 19.2, 22.9.  Between, at two to five CTAs a pair, two would often do:
+    // 64 of 16k-32k, 2 x 256, 163.9, 166.8; 32 of 8k-32k, 8 x 64, 89.7, 93.1; 32 of 200-3000, 4 x 256,
+    // 22.5, 23.8; but 4 of 60k-131k, 4 x 128, 48.8, 46.6.
     const dim3 heads((unsigned)(p.B * p.H));
     if ((int64_t)p.B * p.G * 2 <= n_ctas)
         return launch_early(qdecode_combine_kernel<D, 8>, heads, dim3(256), 0, stream, p, n_ctas);

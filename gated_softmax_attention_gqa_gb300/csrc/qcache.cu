@@ -483,9 +483,12 @@ __global__ void __launch_bounds__(32 * kWarps)
 // KV heads of a block, warps that share a token's heads.  A call too small to fill the device
 // with one warp for all heads of its tokens spreads the heads, over a block's warps first.
 // Passes of a write: their set-up weighs the more the fewer heads follow it, and as they
-// grow the warps get few.  131072 tokens of 2 x 256 take 92 us with two, 87 with four, 86
-// with eight; 40000 30.5, 27.0, 26.2 and 28.7 with one, two, four and eight, 12000 10.5, 9.5,
-// 11.1, 16.3; 32000 of 8 x 128 36.0, 36.9, 40.8, 52.3.
+// grow the warps get few.  us with one, two, four and eight (at one KV head of 64, four is the most):
+//   2 x 256  12000 tokens 10.4  9.3 11.1 16.0   40000 31.3 27.8 27.0 29.2   131072 91.1 78.0 72.1 72.1
+//   1 x 256  10000         7.1  6.5  7.5 10.4   33000 17.9 15.0 14.3 14.9   120000 59.6 48.7 43.0 41.9
+//   1 x 128  20000         8.9  8.5 11.1 17.1   65000 22.6 20.7 21.3 22.7   240000 78.2 68.7 64.9 65.8
+//   1 x 64   40000         7.9  7.5  9.1       130000 20.5 18.2 17.8        500000 73.5 62.7 57.7
+//   8 x 128  32000        36.2 37.2 41.1 53.2
 // A read has little set-up and one pass is best (211k tokens of 4 x 128 86.6 us, 88.4 with two,
 // 97.5 with four; in fp32 150.8, 158.0, 177.4), but for long calls whose rows are long to read and
 // short to write (131072 tokens of 2 x 256 in bf16: 57.8 with one, 54.0 with two).  It has no
