@@ -103,3 +103,28 @@ def test_nan_query_and_masked_nan():
     keep = [h for h in range(H) if h != 2]
     assert torch.equal(out.view(2, H, d)[0], clean.view(2, H, d)[0])
     assert torch.equal(out.view(2, H, d)[1, keep], clean.view(2, H, d)[1, keep])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_nan_stays_in_its_piece(d):
+    """Many short sequences, several (sequence, KV head) pieces to a CTA: a NaN key or value of one
+    leaves those ahead of it and behind it alone."""
+    H, G, rd, base, B = 4, 2, 32, 1e4, 900
+    lens = [1 + 37 * b % 70 for b in range(B)]
+    x = decode_inputs(H, G, d, rd, base, 16, lens, seed=d)
+    clean = run_decode(x, d, rd, base).view(B, H, d)
+    x["table"] = x["table"].cpu()
+    want = torch.zeros(B, H, d, dtype=torch.bool)
+    for b in range(0, B, 7):
+        spoil(x, 0, b, b & 1, lens[b] - 1, 0)
+        want[b, 2 * (b & 1):2 * (b & 1) + 2] = True
+    for b in range(3, B, 7):
+        spoil(x, 1, b, b & 1, lens[b] // 2, 1)
+        want[b, 2 * (b & 1):2 * (b & 1) + 2, 32:64] = True
+    x["table"] = x["table"].to(DEV)
+    out = run_decode(x, d, rd, base).view(B, H, d)
+    torch.cuda.synchronize()
+    assert gattn_get_device_status() == 0
+    want = want.to(DEV)
+    assert torch.equal(out.isnan(), want)
+    assert torch.equal(out[~want], clean[~want])
